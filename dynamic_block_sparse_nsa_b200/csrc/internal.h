@@ -16,6 +16,8 @@ enum : unsigned {
   kErrTimeout = 1u,     // a bounded wait gave up
   kErrSeqLen = 2u,      // a decode sequence length outside [1, T]
   kErrAppendPos = 4u,   // an append position outside [0, T)
+  kErrPage = 8u,        // a page number outside the pool
+  kErrOffsets = 16u,    // token offsets out of order or outside the call's rows
 };
 
 // Arguments of the generic (CUDA-core) NSA row kernel, used for prefill and
@@ -149,6 +151,57 @@ cudaError_t launch_append_bounds(const nsa_params& p, const void* k_new, const i
 size_t quest_ws_bytes(const nsa_params& p);
 cudaError_t launch_quest_select(const nsa_params& p, const void* q, const void* k, int32_t* sel,
                                 void* ws, cudaStream_t stream);
+
+// The 8-bit paged cache (q8_append.cu, q8_attend.cu).
+struct Q8AppendArgs {
+  const void* k_new;        // [N, Hkv, d]
+  const void* v_new;
+  const void* q;            // [N, Hq, d] or NULL
+  const int32_t* pos;       // [B]
+  const int32_t* cu;        // [B + 1] or NULL: one token per sequence
+  const float* rope;        // [rope_len, 2, rot / 2]
+  void* q_out;
+  void* k_out;              // [N, Hkv, d] or NULL
+  void* v_out;
+  uint8_t* k_pages;         // [num_pages, Hkv, page, d] e4m3
+  uint8_t* v_pages;
+  float* k_scale;           // [num_pages, Hkv]
+  float* v_scale;
+  const int32_t* table;     // [B, max_pages]
+  unsigned* err;
+  int B, N, T, Hq, Hkv, d, page, num_pages, max_pages;
+  int rope_len, rot, style;
+};
+cudaError_t launch_q8_append(const Q8AppendArgs& a, nsa_dtype dtype, cudaStream_t stream);
+
+constexpr int kQ8MaxBlocks = 160;  // blocks of a resident grid the workspace has slots for
+struct Q8AttendArgs {
+  const void* q;            // [N, Hq, d]
+  const int32_t* cu;        // [B + 1] or NULL: one query per sequence
+  const int32_t* seq_lens;  // [B]
+  const int32_t* sel;       // [B, Hkv, n] (KEYS_BLOCKS)
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  void* out;                // [N, Hq, d]
+  float* lse;               // [N, Hq] or NULL
+  unsigned* err;
+  int B, N, T, Hq, Hkv, G, page, num_pages, max_pages;
+  int keys, window, n;
+  float scale_log2;         // softmax scale * log2(e)
+  // filled by the launcher
+  float* part;              // partials, two per block
+  float* hold;              // one per warp
+  void* meta;               // per block: what q8_merge joins
+  long* plan_pre;           // NULL: each block makes the plan itself
+  int* plan_seq;
+  int* plan_base;
+  int tiles, rt, blocks, min_chunks;
+};
+size_t q8_attend_ws_bytes(const nsa_params& p, bool ragged);
+cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cudaStream_t stream);
 
 // Kernel trace: bracket a launch with events when tracing is on.
 void trace_begin(const char* name, cudaStream_t stream);

@@ -145,6 +145,56 @@ nsa_status check_workspace(void* ws, size_t have, size_t need) {
   return NSA_OK;
 }
 
+// ---- 8-bit paged cache ----
+
+bool aligned16(const void* x) { return (uintptr_t)x % 16 == 0; }
+
+nsa_status check_q8(const nsa_params* p) {
+  nsa_status s = check_common(p);
+  if (s != NSA_OK) return s;
+  if (p->sel_block != 16 && p->sel_block != 32 && p->sel_block != 64 && p->sel_block != 128)
+    return fail(NSA_ERR_UNSUPPORTED, "pages have 16, 32, 64 or 128 tokens (got sel_block %d)",
+                p->sel_block);
+  if (p->T > (1 << 30)) return fail(NSA_ERR_UNSUPPORTED, "T must be <= 2^30");
+  if (p->window < 1 || p->top_n < 1)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "window and top_n must be >= 1");
+  if (p->top_n > 1024) return fail(NSA_ERR_UNSUPPORTED, "top_n must be <= 1024");
+  return NSA_OK;
+}
+
+nsa_status check_q8_cache(const nsa_q8_cache* c) {
+  if (!c) return fail(NSA_ERR_INVALID_ARGUMENT, "cache is NULL");
+  if (!c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->page_table)
+    return fail(NSA_ERR_INVALID_ARGUMENT,
+                "k_pages, v_pages, k_scale, v_scale, page_table must be non-NULL");
+  if (c->num_pages < 1) return fail(NSA_ERR_INVALID_ARGUMENT, "num_pages must be >= 1");
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages))
+    return fail(NSA_ERR_INVALID_ARGUMENT, "k_pages and v_pages must be 16-byte aligned");
+  return NSA_OK;
+}
+
+Q8AttendArgs q8_attend_args(const nsa_params* p, const nsa_q8_cache* c, int keys) {
+  Q8AttendArgs a{};
+  a.k_pages = (const uint8_t*)c->k_pages;
+  a.v_pages = (const uint8_t*)c->v_pages;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.table = c->page_table;
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.G = p->Hq / p->Hkv;
+  a.page = p->sel_block;
+  a.num_pages = c->num_pages;
+  a.max_pages = (p->T + p->sel_block - 1) / p->sel_block;
+  a.keys = keys;
+  a.window = p->window;
+  a.n = p->top_n;
+  a.scale_log2 = eff_scale(p) * 1.4426950408889634f;
+  return a;
+}
+
 }  // namespace
 
 void set_last_error(nsa_status, const char* msg) { g_detail = msg ? msg : ""; }
@@ -187,6 +237,13 @@ nsa_status nsa_workspace_size(const nsa_params* p, int op, size_t* bytes) {
       nsa_status s = check_nsa(p);
       if (s != NSA_OK) return s;
       *bytes = nsa_bwd_ws_bytes(*p);
+      return NSA_OK;
+    }
+    case NSA_OP_DECODE_Q8:
+    case NSA_OP_PREFILL_Q8: {
+      nsa_status s = check_q8(p);
+      if (s != NSA_OK) return s;
+      *bytes = q8_attend_ws_bytes(*p, op == NSA_OP_PREFILL_Q8);
       return NSA_OK;
     }
     case NSA_OP_MOBA_PREFILL: {
@@ -422,6 +479,10 @@ nsa_status nsa_check(void* stream) {
     return fail(NSA_ERR_INVALID_ARGUMENT, "a decode sequence length was outside [1, T]");
   if (word & kErrAppendPos)
     return fail(NSA_ERR_INVALID_ARGUMENT, "an append position was outside [0, T)");
+  if (word & kErrPage)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "a page number was outside [0, num_pages)");
+  if (word & kErrOffsets)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "token offsets were out of order or out of range");
   return NSA_OK;
 }
 
@@ -440,6 +501,140 @@ nsa_status nsa_append_kv(const nsa_params* p, const void* k_new, const void* v_n
   cudaError_t e = launch_append(*p, k_new, v_new, pos, k_cache, v_cache, w_cmp, k_cmp, v_cmp, err,
                                 (cudaStream_t)stream);
   return e == cudaSuccess ? NSA_OK : cuda_fail(e, "append launch");
+}
+
+nsa_status nsa_append_q8(const nsa_params* p, const nsa_q8_cache* cache, const void* k_new,
+                         const void* v_new, int N, const int32_t* pos, const int32_t* cu_new,
+                         const nsa_rope* rope, const void* q, void* q_out, void* k_out,
+                         void* v_out, void* stream) {
+  g_detail.clear();
+  nsa_status s = check_q8(p);
+  if (s != NSA_OK) return s;
+  s = check_q8_cache(cache);
+  if (s != NSA_OK) return s;
+  if (N < 0 || (!cu_new && N != p->B))
+    return fail(NSA_ERR_INVALID_ARGUMENT, "N must be >= 0, and B (%d) without cu_new (got %d)",
+                p->B, N);
+  if (rope) {
+    if (rope->dim < 16 || rope->dim % 16 != 0 || rope->dim > p->d)
+      return fail(NSA_ERR_UNSUPPORTED,
+                  "the rotated dimension must be a multiple of 16 and at most d (got %d)", rope->dim);
+    if (rope->style != NSA_ROPE_HALF && rope->style != NSA_ROPE_PAIRS)
+      return fail(NSA_ERR_INVALID_ARGUMENT, "unknown rotation style %d", rope->style);
+    if (!rope->table || rope->len < 1 || !aligned16(rope->table))
+      return fail(NSA_ERR_INVALID_ARGUMENT,
+                  "the rotation table must be non-NULL, 16-byte aligned and not empty");
+  }
+  if (N == 0) return NSA_OK;  // nothing to write
+  if (!k_new || !v_new || !pos)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "k_new, v_new, pos must be non-NULL");
+  if (!q != !q_out) return fail(NSA_ERR_INVALID_ARGUMENT, "q and q_out go together");
+  if (!k_out != !v_out) return fail(NSA_ERR_INVALID_ARGUMENT, "k_out and v_out go together");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(q_out) ||
+      !aligned16(k_out) || !aligned16(v_out))
+    return fail(NSA_ERR_INVALID_ARGUMENT, "k_new, v_new, q and the outputs must be 16-byte aligned");
+  if ((long)N * p->Hq > (1l << 37) || ((long)N / p->sel_block + 2l * p->B) * p->Hkv > (1l << 29))
+    return fail(NSA_ERR_UNSUPPORTED, "too many tokens and heads for one call");
+  unsigned* err = err_word(&s);
+  if (!err) return s;
+  Q8AppendArgs a{};
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.q = q;
+  a.pos = pos;
+  a.cu = cu_new;
+  if (rope) {
+    a.rope = rope->table;
+    a.rope_len = rope->len;
+    a.rot = rope->dim;
+    a.style = rope->style;
+  }
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_pages = (uint8_t*)cache->k_pages;
+  a.v_pages = (uint8_t*)cache->v_pages;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.table = cache->page_table;
+  a.err = err;
+  a.B = p->B;
+  a.N = N;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.d = p->d;
+  a.page = p->sel_block;
+  a.num_pages = cache->num_pages;
+  a.max_pages = (p->T + p->sel_block - 1) / p->sel_block;
+  cudaError_t e = launch_q8_append(a, p->dtype, (cudaStream_t)stream);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "append launch");
+}
+
+nsa_status nsa_decode_q8(const nsa_params* p, const nsa_q8_cache* cache, const void* q,
+                         const int32_t* seq_lens, int keys, const int32_t* sel_idx, void* out,
+                         float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  g_detail.clear();
+  nsa_status s = check_q8(p);
+  if (s != NSA_OK) return s;
+  s = check_q8_cache(cache);
+  if (s != NSA_OK) return s;
+  if (keys != NSA_KEYS_ALL && keys != NSA_KEYS_WINDOW && keys != NSA_KEYS_BLOCKS)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "unknown key set %d", keys);
+  if (!q || !seq_lens || !out || (keys == NSA_KEYS_BLOCKS && !sel_idx))
+    return fail(NSA_ERR_INVALID_ARGUMENT, "q, seq_lens, out (and sel_idx for blocks) must be non-NULL");
+  if (!aligned16(q) || !aligned16(out))
+    return fail(NSA_ERR_INVALID_ARGUMENT, "q and out must be 16-byte aligned");
+  s = check_workspace(workspace, ws_bytes, q8_attend_ws_bytes(*p, false));
+  if (s != NSA_OK) return s;
+  unsigned* err = err_word(&s);
+  if (!err) return s;
+  Q8AttendArgs a = q8_attend_args(p, cache, keys);
+  a.q = q;
+  a.seq_lens = seq_lens;
+  a.sel = sel_idx;
+  a.out = out;
+  a.lse = lse;
+  a.err = err;
+  a.N = p->B;
+  cudaError_t e = launch_q8_attend(*p, a, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "decode launch");
+}
+
+nsa_status nsa_prefill_q8(const nsa_params* p, const nsa_q8_cache* cache, const void* q, int N,
+                          const int32_t* cu_q, const int32_t* seq_lens, int keys, void* out,
+                          float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  g_detail.clear();
+  nsa_status s = check_q8(p);
+  if (s != NSA_OK) return s;
+  s = check_q8_cache(cache);
+  if (s != NSA_OK) return s;
+  if (keys != NSA_KEYS_ALL && keys != NSA_KEYS_WINDOW)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "the key set of a prefill is all or window (got %d)", keys);
+  if (N < 0 || (!cu_q && N != p->B) || (long)N > (long)p->B * p->T)
+    return fail(NSA_ERR_INVALID_ARGUMENT,
+                "N must be in [0, B * T], and B (%d) without cu_q (got %d)", p->B, N);
+  if ((long)N * p->Hq > (1l << 34))
+    return fail(NSA_ERR_UNSUPPORTED, "too many tokens and heads for one call");
+  if (N == 0) return NSA_OK;  // nothing to write
+  if (!q || !seq_lens || !out)
+    return fail(NSA_ERR_INVALID_ARGUMENT, "q, seq_lens, out must be non-NULL");
+  if (!aligned16(q) || !aligned16(out))
+    return fail(NSA_ERR_INVALID_ARGUMENT, "q and out must be 16-byte aligned");
+  s = check_workspace(workspace, ws_bytes, q8_attend_ws_bytes(*p, true));
+  if (s != NSA_OK) return s;
+  unsigned* err = err_word(&s);
+  if (!err) return s;
+  Q8AttendArgs a = q8_attend_args(p, cache, keys);
+  a.q = q;
+  a.cu = cu_q;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.err = err;
+  a.N = N;
+  cudaError_t e = launch_q8_attend(*p, a, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "prefill launch");
 }
 
 nsa_status nsa_debug_bounded_wait(const int32_t* flag, int max_iters, void* stream) {

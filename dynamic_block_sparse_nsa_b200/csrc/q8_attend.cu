@@ -1,0 +1,1071 @@
+// Attention over the 8-bit paged cache (nsa_decode_q8, and nsa_prefill_q8 where
+// the tensor-memory kernel does not apply): any group size, page and dtype.
+//
+//   z2 = (q . kcode) * kscale[page] * softmax_scale * log2(e)
+//   o  = sum_keys 2^(z2 - m) * vscale[page] * vcode / sum_keys 2^(z2 - m)
+//
+// One pass with the running maximum m and sum l of each row. A single query's
+// attention reads every live code once and does 4 G flops a byte-pair, so it is
+// bound by HBM; the kernel streams codes and does the products on the warp
+// tensor cores (m16n8k16, 16 query rows of a unit, fp32 accumulators). Codes
+// become halves exactly (e4m3 is a subset of fp16). fp32 rows are kept as two
+// halves each, q = hi + lo and p = hi + lo (22 significant bits), bf16 rows as
+// one: q is scaled by a power of two per row into the top of fp16's range, so
+// its 8 bits stay exact, and p's rounding (2^-12 relative) is below that of
+// the bf16 output (2^-9).
+//
+// A page's value scale multiplies p before p is rounded to half. So that no
+// spread of scales over the pages can push it out of fp16's range, the output
+// has a running reference of its own: o is kept in units of 2^M with M the
+// largest m_page + log2(vscale) so far (less 10, which puts p * vscale in
+// (0, 1024] and its smallest normal 2^-24 below the largest).
+//
+// Each warp streams its own contiguous share of the chunks (32 keys) through a
+// private ring of cp.async stages (no block-wide barrier in the loop); rows
+// outside the sequence, the window or the list are filled with zeros by the
+// copy, so no stale byte reaches a product. Lane (g, t) of a B fragment reads
+// 16 bytes of key g (K: 16 components, the product's k index permuted the same
+// way in q) or the same 16 components of four keys (V), so no transposition is
+// needed; the ring's chunk swizzles make both conflict-free.
+#include <algorithm>
+#include <utility>
+
+#include "q8_attend.cuh"
+
+namespace nsa {
+namespace {
+
+using q8::Seq;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int CK = 32;       // keys per chunk
+constexpr int ROWS = 16;     // query rows per tile
+constexpr int STAGES = 3;
+constexpr int kSmemTiles = 1024;  // tiles whose prefix a block computes itself
+
+template <int D>
+struct Geo {
+  static constexpr int TILE = CK * D;             // bytes of K or V of a chunk
+  static constexpr int RING = STAGES * 2 * TILE;  // a warp's ring
+  static constexpr int PART = ROWS * D + ROWS;    // floats of a partial: o, lse2
+  static_assert(RING >= PART * 4, "a warp's last partial goes into its ring");
+};
+
+struct StageMeta {
+  float ks[2], vs[2];
+  int kb[2];   // position of the page's first key in the chunk
+  int state;   // 0: no key of the chunk is seen; 1: some; 2: every key by every row
+  int pad;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float2 unpack_half(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Byte offset of 16-byte piece c of key r inside a K or V stage. K rows are
+// read eight keys at a time (r, r + 4 in one quarter-warp phase), V rows four
+// (r .. r + 3) with neighbouring pieces.
+template <int D>
+__device__ __forceinline__ uint32_t k_off(int r, int c) {
+  if (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  return ((r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1)) * 64 + (c << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_off(int r, int c) {
+  if (D == 128) return r * 128 + ((c ^ ((r & 3) << 1)) << 4);
+  return r * 64 + ((c ^ (r & 2)) << 4);
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// Where the plan's prefix lives and how a tile maps to its sequence.
+struct Plan {
+  const long* pre;   // chunks (times KV heads) before each tile, [tiles + 1]
+  const int* tseq;   // sequence of each tile; null: tile / rt
+  const int* tbase;  // first tile of each sequence (with tseq)
+  int tiles, rt;
+};
+
+// A place in the list of chunks: (tile, KV head, chunk).
+struct Place {
+  int tile, h, c, nc;
+  __device__ __forceinline__ void init(const Plan& pl, int hkv, long x) {
+    int lo = 0, hi = pl.tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pl.pre[mid] <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    tile = lo;
+    nc = (int)((pl.pre[lo + 1] - pl.pre[lo]) / hkv);
+    const int r = (int)(x - pl.pre[lo]);
+    h = r / nc;
+    c = r - h * nc;
+  }
+  // Next chunk; true when it belongs to another unit.
+  __device__ __forceinline__ bool next(const Plan& pl, int hkv) {
+    if (++c < nc) return false;
+    c = 0;
+    if (++h == hkv) {
+      h = 0;
+      ++tile;
+      if (tile < pl.tiles) nc = (int)((pl.pre[tile + 1] - pl.pre[tile]) / hkv);
+    }
+    return true;
+  }
+};
+
+// A unit's sequence and row range.
+struct Unit {
+  int b, r0, lo, hi;
+  Seq s;
+  __device__ __forceinline__ void load(const Q8AttendArgs& a, const Plan& pl, int tile) {
+    b = pl.tseq ? pl.tseq[tile] : tile / pl.rt;
+    r0 = (tile - (pl.tseq ? pl.tbase[b] : b * pl.rt)) * ROWS;
+    s = q8::sequence(a, b);
+    q8::key_span(a, s, r0, ROWS, lo, hi);
+  }
+};
+
+// The copying side of a warp: its place, the pages ahead of it (one per lane)
+// and the ring.
+template <int D, int PP>
+struct Feeder {
+  Place at;
+  Unit u;
+  int gbase;       // entry held by lane 0
+  int pid, blk;    // this lane's page and its block number; -1: none
+  float ks, vs;
+
+  __device__ __forceinline__ void pages(const Q8AttendArgs& a, int e, int lane) {
+    gbase = e;
+    const int i = e + lane;
+    blk = -1;
+    if (a.keys == q8::KEYS_BLOCKS) {
+      const int32_t* list = a.sel + ((long)u.b * a.Hkv + at.h) * a.n;
+      if (i < a.n) blk = list[i];
+      if (blk < 0 || (long)blk * a.page >= u.hi) blk = -1;
+      // a block listed twice counts once
+      const unsigned same = __match_any_sync(0xffffffffu, blk);
+      if (blk >= 0 && (same & ((1u << lane) - 1))) blk = -1;
+      for (int k = 0; k < e; ++k)
+        if (list[k] == blk) blk = -1;
+    } else if ((long)i * a.page < u.hi) {
+      blk = i;
+    }
+    pid = blk >= 0 ? a.table[(long)u.b * a.max_pages + blk] : -1;
+    if (blk >= 0 && (pid < 0 || pid >= a.num_pages)) {
+      atomicOr(a.err, kErrPage);
+      pid = blk = -1;
+    }
+    ks = vs = 0.f;
+    if (pid >= 0) {
+      ks = a.k_scale[(long)pid * a.Hkv + at.h];
+      vs = a.v_scale[(long)pid * a.Hkv + at.h];
+    }
+  }
+
+  __device__ __forceinline__ void start(const Q8AttendArgs& a, const Plan& pl, long x) {
+    at.init(pl, a.Hkv, x);
+    u.load(a, pl, at.tile);
+    gbase = INT_MIN / 2;
+  }
+
+  // Copies the chunk at the place into a stage, as two groups (K, then V).
+  __device__ __forceinline__ void issue(const Q8AttendArgs& a, unsigned char* stage,
+                                        StageMeta* meta, int lane) {
+    const int ch = at.c + (a.keys == q8::KEYS_BLOCKS ? 0 : u.lo / CK);
+    const long key0 = (long)ch * CK;
+    const int e = (int)(key0 / a.page);
+    const int off = PP == 1 ? (int)(key0 % a.page) : 0;
+    if (e + PP > gbase + 32 || e < gbase) pages(a, e, lane);
+    int p[PP], kb[PP];
+    float kss[PP], vss[PP];
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int src = e - gbase + i;
+      p[i] = __shfl_sync(0xffffffffu, pid, src);
+      kb[i] = __shfl_sync(0xffffffffu, blk, src) * a.page + off;
+      kss[i] = __shfl_sync(0xffffffffu, ks, src);
+      vss[i] = __shfl_sync(0xffffffffu, vs, src);
+      if (p[i] < 0) kb[i] = INT_MAX / 2;  // past every row
+    }
+    if (lane == 0) {
+      // rows of the tile see from the first token's window to the last token's
+      // position; all of them see [full_lo, full_hi)
+      const int t0 = u.r0 / a.G, t1 = min(u.s.n - 1, (u.r0 + ROWS - 1) / a.G);
+      const int at0 = u.s.len - u.s.n;
+      const int full_hi = u.hi > 0 ? at0 + t0 + 1 : 0;
+      const int full_lo = a.keys == q8::KEYS_WINDOW ? at0 + t1 + 1 - a.window : 0;
+      bool some = false, full = true;
+#pragma unroll
+      for (int i = 0; i < PP; ++i) {
+        const int w = CK / PP;
+        some |= kb[i] < u.hi && kb[i] + w > u.lo;
+        full &= kb[i] >= full_lo && kb[i] + w <= full_hi;
+        meta->ks[i] = kss[i];
+        meta->vs[i] = vss[i];
+        meta->kb[i] = kb[i];
+      }
+      meta->state = some ? (full ? 2 : 1) : 0;
+    }
+    constexpr int PIECES = D / 16, RPI = 32 / PIECES;
+    const int c = lane % PIECES, rl = lane / PIECES;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint8_t* base = kv ? a.v_pages : a.k_pages;
+      unsigned char* dst = stage + kv * Geo<D>::TILE;
+#pragma unroll
+      for (int i = 0; i < CK / RPI; ++i) {
+        const int r = i * RPI + rl;
+        const int pi = PP == 1 ? 0 : i * RPI / (CK / PP);  // (a copy's rows lie in one page)
+        const int slot = PP == 1 ? off + r : r % (CK / PP);
+        const int pos = kb[pi] + (PP == 1 ? r : slot);
+        const bool live = pos >= u.lo && pos < u.hi;
+        const uint8_t* src = base;
+        if (live) src += (((long)p[pi] * a.Hkv + at.h) * a.page + slot) * D + c * 16;
+        ptx::cp_async16_zfill(dst + (kv ? v_off<D>(r, c) : k_off<D>(r, c)), src, live ? 16 : 0);
+      }
+      ptx::cp_async_commit();
+    }
+  }
+
+  __device__ __forceinline__ void next(const Q8AttendArgs& a, const Plan& pl) {
+    const int tile = at.tile;
+    if (!at.next(pl, a.Hkv)) return;
+    gbase = INT_MIN / 2;
+    if (at.tile != tile && at.tile < pl.tiles) u.load(a, pl, at.tile);
+  }
+};
+
+// The computing side: a unit's query rows and its running softmax.
+template <typename T, int D>
+struct Rows {
+  static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+  static constexpr int KS = D / 16;  // product steps of 16 components
+  static constexpr int NT = D / 8;   // output tiles of 8 components
+  uint32_t q[PARTS][KS][4];
+  float qf[2];        // row factor of the scores: 2^shift * softmax_scale * log2(e)
+  int lo[2], hi[2];   // keys the lane's two rows see
+  float o[NT][4];
+  float m[2], l[2], M[2];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m[0] = m[1] = M[0] = M[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // Row r of a sequence in q / out: its token's head.
+  static __device__ __forceinline__ long row_of(const Q8AttendArgs& a, const Seq& s, int h, int r) {
+    return ((long)s.first + r / a.G) * a.Hq + h * a.G + r % a.G;
+  }
+
+  __device__ __forceinline__ void load(const Q8AttendArgs& a, const Unit& u, int h, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = u.r0 + g + 8 * i;
+      const bool real = r < u.s.n * a.G;
+      const int pos = u.s.len - u.s.n + r / a.G;
+      hi[i] = real && u.hi > 0 ? pos + 1 : 0;
+      lo[i] = a.keys == q8::KEYS_WINDOW ? max(0, pos + 1 - a.window) : 0;
+      const T* src = static_cast<const T*>(a.q) + (real ? row_of(a, u.s, h, r) : 0) * D;
+      // lane t's components of step 4 half + j are 16 (4 half + t) + 4 j ..
+      float x[D / 4];
+      float big = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        if (real) {
+          q8::Vec8<T>::load(src + 64 * (c >> 1) + 16 * t + 8 * (c & 1), x + 8 * c);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[8 * c + j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 4; ++j)
+        if (fabsf(x[j]) < INFINITY) big = fmaxf(big, fabsf(x[j]));
+      big = quad_max(big);
+      // 2^up brings the largest component to [2^14, 2^15)
+      int up = big > 0.f ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
+      up = min(max(up, -120), 120);
+      const float mul = q8::exp2_int(up);
+      qf[i] = q8::exp2_int(-up) * a.scale_log2;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const float u0 = x[4 * s + 2 * w] * mul, u1 = x[4 * s + 2 * w + 1] * mul;
+          const uint32_t hi2 = pack_half(u0, u1);
+          q[0][s][i + 2 * w] = hi2;
+          if (PARTS == 2) {
+            const float2 f = unpack_half(hi2);
+            // (an infinite component has no second part)
+            q[PARTS - 1][s][i + 2 * w] =
+                pack_half(fabsf(u0) < INFINITY ? u0 - f.x : 0.f, fabsf(u1) < INFINITY ? u1 - f.y : 0.f);
+          }
+        }
+    }
+  }
+
+  // z[nt][.]: scores of keys 8 nt + t, 8 nt + t + 4 for rows g (0, 1) and g + 8 (2, 3)
+  __device__ __forceinline__ void scores(float (&z)[4][4], uint32_t kbase, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int kr = (g >> 1) | ((g & 1) << 2);
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.f;
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        const uint4 v = lds128(kbase + k_off<D>(8 * nt + kr, 4 * half + t));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b0 = q8::e4m3x2_to_half2((uint16_t)(w[j] & 0xffffu));
+          const uint32_t b1 = q8::e4m3x2_to_half2((uint16_t)(w[j] >> 16));
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) mma_f16(z[nt], q[p][4 * half + j], b0, b1);
+        }
+      }
+    }
+  }
+
+  // Running softmax: z becomes p * vscale in units of 2^M; o, l, m, M follow.
+  template <int PP>
+  __device__ __forceinline__ void softmax(float (&z)[4][4], const StageMeta& meta, bool full,
+                                          int lane) {
+    const int t = lane & 3;
+    constexpr int TP = 4 / PP;  // score tiles of a page
+    float lv[PP];               // log2 of the value scales
+#pragma unroll
+    for (int p = 0; p < PP; ++p) lv[p] = __log2f(meta.vs[p]);
+    if (!full) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = x >> 1;
+          const int key = meta.kb[nt / TP] + 8 * (nt % TP) + t + 4 * (x & 1);
+          z[nt][x] = key >= lo[i] && key < hi[i] ? z[nt][x] * (qf[i] * meta.ks[nt / TP]) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[nt][x] *= qf[x >> 1] * meta.ks[nt / TP];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = m[i], ref = M[i];
+#pragma unroll
+      for (int p = 0; p < PP; ++p) {
+        float pm = -INFINITY;
+#pragma unroll
+        for (int nt = p * TP; nt < (p + 1) * TP; ++nt)
+          pm = fmaxf(pm, fmaxf(z[nt][2 * i], z[nt][2 * i + 1]));
+        pm = quad_max(pm);
+        top = fmaxf(top, pm);
+        ref = fmaxf(ref, pm + fmaxf(lv[p], -126.f) - 10.f);
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      const float oref = ref == -INFINITY ? 0.f : ref;
+      const float al = ptx::ex2(m[i] - base), ao = ptx::ex2(M[i] - oref);
+      m[i] = top;
+      M[i] = ref;
+      float sum = 0.f;
+      bool far = false;
+#pragma unroll
+      for (int p = 0; p < PP; ++p) far |= base - oref + lv[p] > 100.f;
+      if (__any_sync(0xffffffffu, far)) {
+        // a page of much larger values than the others' that is hardly
+        // attended: p would leave fp32's range before its scale brings it back
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int x = 2 * i; x < 2 * i + 2; ++x) {
+            sum += ptx::ex2(z[nt][x] - base);
+            z[nt][x] = ptx::ex2(z[nt][x] - oref + lv[nt / TP]);
+          }
+      } else {
+        float f[PP];
+#pragma unroll
+        for (int p = 0; p < PP; ++p) f[p] = ptx::ex2(base - oref + lv[p]);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int x = 2 * i; x < 2 * i + 2; ++x) {
+            const float p = ptx::ex2(z[nt][x] - base);
+            sum += p;
+            z[nt][x] = p * f[nt / TP];
+          }
+      }
+      l[i] = l[i] * al + sum;
+      if (__any_sync(0xffffffffu, ao != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][2 * i] *= ao;
+          o[j][2 * i + 1] *= ao;
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void values(const float (&z)[4][4], uint32_t vbase, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t a[PARTS][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        // a0, a1: rows g, g + 8 of keys t, t + 4; a2, a3: of keys 8 + t, 12 + t
+        const float p0 = z[2 * s + (x >> 1)][2 * (x & 1)], p1 = z[2 * s + (x >> 1)][2 * (x & 1) + 1];
+        a[0][x] = pack_half(p0, p1);
+        if (PARTS == 2) {
+          const float2 f = unpack_half(a[0][x]);
+          a[PARTS - 1][x] = pack_half(p0 - f.x, p1 - f.y);
+        }
+      }
+      uint32_t w[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * s + 4 * i + t;
+        if (D == 128) {
+          const uint4 v = lds128(vbase + v_off<D>(r, g));
+          w[i][0] = v.x;
+          w[i][1] = v.y;
+          w[i][D / 32 - 2] = v.z;
+          w[i][D / 32 - 1] = v.w;
+        } else {
+          const uint2 v = lds64(vbase + v_off<D>(r, g >> 1) + (g & 1) * 8);
+          w[i][0] = v.x;
+          w[i][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t sel = y ? 0x7362u : 0x5140u;
+          const uint32_t x0 = __byte_perm(w[0][k], w[1][k], sel);
+          const uint32_t x1 = __byte_perm(w[2][k], w[3][k], sel);
+          const uint32_t b00 = q8::e4m3x2_to_half2((uint16_t)(x0 & 0xffffu));
+          const uint32_t b01 = q8::e4m3x2_to_half2((uint16_t)(x1 & 0xffffu));
+          const uint32_t b10 = q8::e4m3x2_to_half2((uint16_t)(x0 >> 16));
+          const uint32_t b11 = q8::e4m3x2_to_half2((uint16_t)(x1 >> 16));
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            mma_f16(o[4 * k + 2 * y], a[p], b00, b01);
+            mma_f16(o[4 * k + 2 * y + 1], a[p], b10, b11);
+          }
+        }
+    }
+  }
+
+  // Values that are NaN in keys which some rows of the tile see and others do
+  // not: 0 * NaN must not reach the rows that do not. Their codes become zeros
+  // in the stage and the rows that see them become NaN. Rare, and only in
+  // chunks on the edge of a row's keys.
+  template <int PP>
+  __device__ void nan_values(unsigned char* vst, const StageMeta& meta, int lane) {
+    bool found = false;
+    for (int i = lane; i < CK * D / 16; i += 32) {
+      const uint4 v = reinterpret_cast<const uint4*>(vst)[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) found |= __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    }
+    if (!__any_sync(0xffffffffu, found)) return;
+    const int t = lane & 3;
+    constexpr int RUN = D / 4;  // the lane's outputs are components RUN t .. of its rows
+    for (int r = 0; r < CK; ++r) {
+      const int key = meta.kb[r / (CK / PP)] + r % (CK / PP);
+#pragma unroll
+      for (int j = 0; j < RUN; ++j) {
+        const int dim = RUN * t + j;
+        const uint8_t code = vst[v_off<D>(r, dim / 16) + dim % 16];
+        if ((code & 0x7f) == 0x7f) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (key >= lo[i] && key < hi[i])
+              o[j % NT][2 * i + j / NT] = __uint_as_float(0x7fffffffu);
+        }
+      }
+    }
+    __syncwarp();
+    for (int i = lane; i < CK * D / 4; i += 32) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(vst) + i;
+      *w &= ~__vcmpeq4(*w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    }
+    __syncwarp();
+  }
+
+  // Ends the unit: o normalised, lse2 = log2 of the sum of 2^z2.
+  __device__ __forceinline__ void finish(float (&lse2)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float sum = quad_sum(l[i]);
+      const float base = m[i] == -INFINITY ? 0.f : m[i], oref = M[i] == -INFINITY ? 0.f : M[i];
+      // in two factors: 2^(M - m) alone can leave fp32's range
+      const float half = ptx::ex2(0.5f * (oref - base));
+      const float f = sum == 0.f ? 0.f : half / sum;
+      lse2[i] = sum == 0.f ? -INFINITY : m[i] + log2f(sum);
+      // (a row without keys has o = 0, NaN only where NaN values were marked)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o[j][2 * i] = o[j][2 * i] * half * f;
+        o[j][2 * i + 1] = o[j][2 * i + 1] * half * f;
+      }
+    }
+  }
+
+  // The lane holds components D / 4 * t .. + D / 4 - 1 of its rows: first half
+  // of them in o[.][2 i], second in o[.][2 i + 1].
+  __device__ __forceinline__ void write(const Q8AttendArgs& a, const Unit& u, int h,
+                                        const float (&lse2)[2], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = u.r0 + g + 8 * i;
+      if (r >= u.s.n * a.G) continue;
+      const long row = row_of(a, u.s, h, r);
+      T* dst = static_cast<T*>(a.out) + row * D + (D / 4) * t;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < NT; j += 4) {
+          const float v[4] = {o[j][2 * i + c], o[j + 1][2 * i + c], o[j + 2][2 * i + c],
+                              o[j + 3][2 * i + c]};
+          if (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(dst + NT * c + j) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            *reinterpret_cast<uint2*>(dst + NT * c + j) =
+                make_uint2(ptx::pack_bf16(v[0], v[1]), ptx::pack_bf16(v[2], v[3]));
+          }
+        }
+      if (t == 0 && a.lse) a.lse[row] = lse2[i] * q8::kLn2;
+    }
+  }
+
+  __device__ __forceinline__ void store(float* part, const float (&lse2)[2], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float* dst = part + (g + 8 * i) * D + (D / 4) * t;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < NT; j += 4)
+          *reinterpret_cast<float4*>(dst + NT * c + j) =
+              make_float4(o[j][2 * i + c], o[j + 1][2 * i + c], o[j + 2][2 * i + c],
+                          o[j + 3][2 * i + c]);
+      if (t == 0) part[ROWS * D + g + 8 * i] = lse2[i];
+    }
+  }
+};
+
+// A warp's unfinished unit: begun before its share or continued behind it.
+struct Segment {
+  int tile, h;       // tile -1: none
+  const float* part;
+};
+
+template <typename T, int D>
+struct Smem {
+  static constexpr int RING = kWarps * Geo<D>::RING;
+  static constexpr int META = RING;
+  static constexpr int SEGS = META + kWarps * STAGES * (int)sizeof(StageMeta);
+  static constexpr int SUMS = SEGS + 2 * kWarps * (int)sizeof(Segment);
+  static constexpr int PRE = SUMS + kWarps * 8;
+  static constexpr int BYTES = PRE + (kSmemTiles + 1) * 8;
+};
+
+template <typename T, int D, int PP>
+__global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const Q8AttendArgs a) {
+  using S = Smem<T, D>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+
+  // ---- plan ----
+  Plan pl;
+  pl.tiles = a.tiles;
+  pl.rt = a.rt;
+  pl.tseq = nullptr;
+  pl.tbase = nullptr;
+  if (a.plan_pre) {
+    pl.pre = a.plan_pre;
+    pl.tseq = a.plan_seq;
+    pl.tbase = a.plan_base;
+    pl.tiles = a.plan_base[a.B];
+  } else {
+    long* pre = reinterpret_cast<long*>(smem + S::PRE);
+    long* sums = reinterpret_cast<long*>(smem + S::SUMS);
+    long base = 0;
+    if (tid == 0) pre[0] = 0;
+    for (int t0 = 0; t0 < a.tiles; t0 += kThreads) {
+      const int tile = t0 + tid;
+      long mine = 0;
+      if (tile < a.tiles) {
+        const int b = tile / a.rt;
+        const Seq s = q8::sequence(a, b);
+        if (!s.ok && blockIdx.x == 0) atomicOr(a.err, s.err);
+        mine = (long)q8::chunks_of(a, s, (tile - b * a.rt) * ROWS, ROWS, CK) * a.Hkv;
+      }
+      long run = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long up = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += up;
+      }
+      if (lane == 31) sums[warp] = run;
+      __syncthreads();
+      long before = base;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        if (k < warp) before += sums[k];
+        base += sums[k];
+      }
+      if (tile < a.tiles) pre[tile + 1] = before + run;
+      __syncthreads();
+    }
+    __syncthreads();
+    pl.pre = pre;
+  }
+  if (tid < 2 * kWarps) segs[tid].tile = -1;
+  __syncthreads();
+  const long V = pl.tiles ? pl.pre[pl.tiles] : 0;
+  // few chunks: fewer blocks, so that a block's warps share its merge
+  const long want = (V + a.min_chunks - 1) / a.min_chunks;
+  const int C = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
+  const int cta = blockIdx.x;
+  q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
+  if (cta >= C || V == 0) {
+    if (tid == 0) mm[cta].unit = -1;
+    return;
+  }
+  const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
+  const long x0 = X0 + (X1 - X0) * warp / kWarps, x1 = X0 + (X1 - X0) * (warp + 1) / kWarps;
+
+  if (x1 > x0) {
+    unsigned char* ring = smem + warp * Geo<D>::RING;
+    StageMeta* meta = reinterpret_cast<StageMeta*>(smem + S::META) + warp * STAGES;
+    const uint32_t ring_u = ptx::smem_u32(ring);
+    Feeder<D, PP> feed;
+    feed.start(a, pl, x0);
+    long fx = x0;
+    Place at = feed.at;
+    Unit u = feed.u;
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) {
+      if (fx < x1) {
+        feed.issue(a, ring + k * 2 * Geo<D>::TILE, meta + k, lane);
+        if (++fx < x1) feed.next(a, pl);
+      } else {
+        ptx::cp_async_commit();
+        ptx::cp_async_commit();
+      }
+    }
+    Rows<T, D> rows;
+    rows.load(a, u, at.h, lane);
+    rows.clear();
+    bool whole = at.c == 0;  // the unit's first chunk is the warp's
+    int st = 0;
+    for (long x = x0; x < x1; ++x) {
+      ptx::cp_async_wait<2 * (STAGES - 2) + 1>();
+      __syncwarp();
+      const int nx = st == 0 ? STAGES - 1 : st - 1;
+      if (fx < x1) {
+        feed.issue(a, ring + nx * 2 * Geo<D>::TILE, meta + nx, lane);
+        if (++fx < x1) feed.next(a, pl);
+      } else {
+        ptx::cp_async_commit();
+        ptx::cp_async_commit();
+      }
+      const StageMeta sm = meta[st];
+      float z[4][4];
+      if (sm.state) {
+        rows.scores(z, ring_u + st * 2 * Geo<D>::TILE, lane);
+        rows.template softmax<PP>(z, sm, sm.state == 2, lane);
+      }
+      ptx::cp_async_wait<2 * (STAGES - 1)>();
+      __syncwarp();
+      if (sm.state) {
+        const uint32_t vb = ring_u + st * 2 * Geo<D>::TILE + Geo<D>::TILE;
+        if (sm.state == 1 && a.cu)
+          rows.template nan_values<PP>(ring + st * 2 * Geo<D>::TILE + Geo<D>::TILE, sm, lane);
+        rows.values(z, vb, lane);
+      }
+      st = st + 1 == STAGES ? 0 : st + 1;
+      const bool last = at.c + 1 == at.nc;
+      if (last || x + 1 == x1) {
+        float lse2[2];
+        rows.finish(lse2);
+        if (whole && last) {
+          rows.write(a, u, at.h, lse2, lane);
+        } else if (x + 1 < x1) {
+          float* part = a.hold + ((long)cta * kWarps + warp) * Geo<D>::PART;
+          rows.store(part, lse2, lane);
+          if (lane == 0) segs[2 * warp] = Segment{at.tile, at.h, part};
+        } else {
+          ptx::cp_async_wait<0>();
+          __syncwarp();  // the ring is free
+          float* part = reinterpret_cast<float*>(ring);
+          rows.store(part, lse2, lane);
+          if (lane == 0) segs[2 * warp + 1] = Segment{at.tile, at.h, part};
+        }
+        if (x + 1 < x1) {
+          const int tile = at.tile;
+          at.next(pl, a.Hkv);
+          if (at.tile != tile) u.load(a, pl, at.tile);
+          rows.load(a, u, at.h, lane);
+          rows.clear();
+          whole = true;
+        }
+      } else {
+        ++at.c;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- join the block's segments of each unit ----
+  long head = -1;  // unit in the block's first slot
+  int from = 0;
+  for (int k = 0; k < 2 * kWarps;) {
+    const int tile = segs[k].tile, h = segs[k].h;
+    if (tile < 0) {
+      ++k;
+      continue;
+    }
+    int end = k + 1;  // segments k .. end - 1 (with gaps) are of one unit
+    for (int e = k + 1; e < 2 * kWarps; ++e) {
+      if (segs[e].tile < 0) continue;
+      if (segs[e].tile != tile || segs[e].h != h) break;
+      end = e + 1;
+    }
+    const int nc = (int)((pl.pre[tile + 1] - pl.pre[tile]) / a.Hkv);
+    const long u0 = pl.pre[tile] + (long)h * nc, u1 = u0 + nc;
+    const bool done = u0 >= X0 && u1 <= X1;
+    float* slot = a.part + (2l * cta + (u0 < X0 ? 0 : 1)) * Geo<D>::PART;
+    if (!done) {
+      if (u0 < X0) {
+        head = (long)tile * a.Hkv + h;
+        from = u1 <= X1 ? q8::block_of(u0, V, C) : -1;
+      }
+    }
+    Unit u;
+    if (done) u.load(a, pl, tile);
+#pragma unroll
+    for (int rr = 0; rr < ROWS / kWarps; ++rr) {
+      const int r = warp * (ROWS / kWarps) + rr;
+      float top = -INFINITY;
+      for (int e = k; e < end; ++e)
+        if (segs[e].tile >= 0) top = fmaxf(top, segs[e].part[ROWS * D + r]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float acc[D / 32], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+      for (int e = k; e < end; ++e) {
+        if (segs[e].tile < 0) continue;
+        const float* p = segs[e].part;
+        const float wgt = ptx::ex2(p[ROWS * D + r] - base);
+        sum += wgt;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] += wgt * p[r * D + i * 32 + lane];
+      }
+      const float f = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+      if (!done) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) slot[r * D + i * 32 + lane] = acc[i] * f;
+        if (lane == 0) slot[ROWS * D + r] = lse2;
+      } else if (u.r0 + r < u.s.n * a.G) {
+        const long row = Rows<T, D>::row_of(a, u.s, h, u.r0 + r);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          static_cast<T*>(a.out)[row * D + i * 32 + lane] = from_f32<T>(acc[i] * f);
+        if (lane == 0 && a.lse) a.lse[row] = lse2 * q8::kLn2;
+      }
+    }
+    k = end;
+  }
+  if (tid == 0) {
+    mm[cta].unit = head >= 0 && from >= 0 ? head : -1;
+    mm[cta].from = from;
+  }
+}
+
+// Joins the partials of a unit that lies in several blocks: block (c, r) does
+// row r of the unit that ends in attention block c, from slot 2 f + 1 of the
+// block f it begins in and slots 2 i of the blocks behind it up to c.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) q8_merge_kernel(const Q8AttendArgs a, int tile_rows) {
+  constexpr int V = D / 32;
+  ptx::grid_dep_wait();
+  const q8::MergeMeta mm = reinterpret_cast<const q8::MergeMeta*>(a.meta)[blockIdx.x];
+  if (mm.unit < 0) return;
+  const int tile = (int)(mm.unit / a.Hkv), h = (int)(mm.unit % a.Hkv), r = blockIdx.y;
+  const int b = a.plan_pre ? a.plan_seq[tile] : tile / a.rt;
+  const int r0 = (tile - (a.plan_pre ? a.plan_base[b] : b * a.rt)) * tile_rows;
+  const Seq s = q8::sequence(a, b);
+  if (r0 + r >= s.n * a.G) return;
+  const long stride = (long)tile_rows * (D + 1);
+  const int n = (int)blockIdx.x - mm.from + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto part = [&](int i) { return a.part + (2l * (mm.from + i) + (i == 0 ? 1 : 0)) * stride; };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[tile_rows * D + r]);
+  top = warp_max(top);
+  const float base = top == -INFINITY ? 0.f : top;
+  float acc[V], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += 4) {
+    const float* p = part(i);
+    const float w = ptx::ex2(p[tile_rows * D + r] - base);
+    sum += w;
+    if (V == 4) {
+      const float4 x = reinterpret_cast<const float4*>(p + r * D)[lane];
+      acc[0] += w * x.x;
+      acc[1] += w * x.y;
+      acc[V - 2] += w * x.z;
+      acc[V - 1] += w * x.w;
+    } else {
+      const float2 x = reinterpret_cast<const float2*>(p + r * D)[lane];
+      acc[0] += w * x.x;
+      acc[1] += w * x.y;
+    }
+  }
+  __shared__ float s_acc[4][D], s_sum[4];
+#pragma unroll
+  for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  const int dim = threadIdx.x;
+  const float all = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  const long row = Rows<T, D>::row_of(a, s, h, r0 + r);
+  if (dim < D) {
+    const float v = s_acc[0][dim] + s_acc[1][dim] + s_acc[2][dim] + s_acc[3][dim];
+    static_cast<T*>(a.out)[row * D + dim] = from_f32<T>(all == 0.f ? 0.f : v / all);
+  }
+  if (dim == 0 && a.lse) a.lse[row] = all == 0.f ? -INFINITY : (top + log2f(all)) * q8::kLn2;
+}
+
+// The plan of a call with offsets, or of more tiles than a block takes in: the
+// tiles of every sequence and the chunks before each tile. One block.
+constexpr int kPlanThreads = 1024;
+template <typename I>
+__device__ __forceinline__ I block_scan(I mine, I* sums, I& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  I run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I up = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += up;
+  }
+  if (lane == 31) sums[warp] = run;
+  __syncthreads();
+  I before = 0;
+  total = 0;
+  for (int k = 0; k < kPlanThreads / 32; ++k) {
+    if (k < warp) before += sums[k];
+    total += sums[k];
+  }
+  __syncthreads();
+  return before + run - mine;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArgs a, int tile_rows,
+                                                               int chunk) {
+  __shared__ long sums[kPlanThreads / 32];
+  ptx::grid_dep_wait();
+  const int tid = threadIdx.x;
+  long base = 0, all;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long mine = 0;
+    if (b < a.B) {
+      const Seq s = q8::sequence(a, b);
+      if (!s.ok) atomicOr(a.err, s.err);
+      mine = q8::tiles_of(a, s.n, tile_rows);
+    }
+    const long at = block_scan(mine, sums, all);
+    if (b < a.B) {
+      a.plan_base[b] = (int)(base + at);
+      for (long k = 0; k < mine; ++k)
+        if (base + at + k < a.tiles) a.plan_seq[base + at + k] = b;
+    }
+    base += all;
+  }
+  const int tiles = (int)(base < a.tiles ? base : a.tiles);
+  if (tid == 0) {
+    a.plan_base[a.B] = tiles;
+    a.plan_pre[0] = 0;
+  }
+  __syncthreads();
+  base = 0;
+  for (int t0 = 0; t0 < tiles; t0 += kPlanThreads) {
+    const int t = t0 + tid;
+    long mine = 0;
+    if (t < tiles) {
+      const int b = a.plan_seq[t];
+      const Seq s = q8::sequence(a, b);
+      mine = (long)q8::chunks_of(a, s, (t - a.plan_base[b]) * tile_rows, tile_rows, chunk) * a.Hkv;
+    }
+    const long at = block_scan(mine, sums, all);
+    if (t < tiles) a.plan_pre[t + 1] = base + at + mine;
+    base += all;
+  }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+template <typename T, int D, int PP>
+cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
+  auto kern = q8_attend_kernel<T, D, PP>;
+  constexpr int smem = Smem<T, D>::BYTES;
+  cudaError_t e;
+  if ((e = ensure_dyn_smem((const void*)kern, smem)) != cudaSuccess) return e;
+  {
+    TraceScope trace("q8_attend", stream);
+    if ((e = launch_pdl(kern, dim3(a.blocks), dim3(kThreads), smem, stream, a)) != cudaSuccess)
+      return e;
+  }
+  TraceScope trace("q8_merge", stream);
+  return launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, ROWS), dim3(128), 0, stream, a, ROWS);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Most tiles a call can have; N is the number of query tokens.
+long most_tiles(const nsa_params& p, bool ragged, long N) {
+  const int G = p.Hq / p.Hkv;
+  if (!ragged) return (long)p.B * ((G + ROWS - 1) / ROWS);
+  return N * G / ROWS + p.B;
+}
+
+struct Layout {
+  size_t part, hold, meta, pre, seq, base, total;
+};
+
+// (sized for the most query tokens the parameters allow, B * T)
+Layout layout(const nsa_params& p, bool ragged) {
+  Layout L{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  };
+  const size_t part = (size_t)(ROWS * p.d + ROWS) * 4;
+  L.part = take(part * 2 * kQ8MaxBlocks);
+  L.hold = take(part * kWarps * kQ8MaxBlocks);
+  L.meta = take(sizeof(q8::MergeMeta) * kQ8MaxBlocks);
+  const long tiles = most_tiles(p, ragged, (long)p.B * p.T);
+  if (ragged || tiles > kSmemTiles) {
+    L.pre = take((size_t)(tiles + 1) * 8);
+    L.seq = take((size_t)tiles * 4);
+    L.base = take((size_t)(p.B + 1) * 4);
+  }
+  L.total = at;
+  return L;
+}
+
+}  // namespace
+
+size_t q8_attend_ws_bytes(const nsa_params& p, bool ragged) {
+  return layout(p, ragged).total;
+}
+
+cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cudaStream_t stream) {
+  const bool ragged = a.cu != nullptr;
+  const Layout L = layout(p, ragged);
+  char* w = static_cast<char*>(ws);
+  a.part = reinterpret_cast<float*>(w + L.part);
+  a.hold = reinterpret_cast<float*>(w + L.hold);
+  a.meta = w + L.meta;
+  a.tiles = (int)most_tiles(p, ragged, a.N);
+  a.rt = (a.G + ROWS - 1) / ROWS;
+  a.blocks = std::min(device_sm_count(), kQ8MaxBlocks);
+  a.min_chunks = 8;
+  a.plan_pre = nullptr;
+  a.plan_seq = nullptr;
+  a.plan_base = nullptr;
+  if (ragged || a.tiles > kSmemTiles) {
+    a.plan_pre = reinterpret_cast<long*>(w + L.pre);
+    a.plan_seq = reinterpret_cast<int*>(w + L.seq);
+    a.plan_base = reinterpret_cast<int*>(w + L.base);
+    TraceScope trace("q8_plan", stream);
+    const cudaError_t e = launch_pdl(q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a,
+                                     ROWS, CK);
+    if (e != cudaSuccess) return e;
+  }
+  const bool bf16 = p.dtype == NSA_DTYPE_BF16;
+  using bf = __nv_bfloat16;
+  if (p.d == 128) {
+    if (a.page >= CK)
+      return bf16 ? launch<bf, 128, 1>(a, stream) : launch<float, 128, 1>(a, stream);
+    return bf16 ? launch<bf, 128, 2>(a, stream) : launch<float, 128, 2>(a, stream);
+  }
+  if (a.page >= CK) return bf16 ? launch<bf, 64, 1>(a, stream) : launch<float, 64, 1>(a, stream);
+  return bf16 ? launch<bf, 64, 2>(a, stream) : launch<float, 64, 2>(a, stream);
+}
+
+}  // namespace nsa

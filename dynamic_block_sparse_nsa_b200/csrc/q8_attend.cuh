@@ -1,0 +1,95 @@
+// Work plan shared by the attention kernels over the 8-bit paged cache.
+//
+// A "tile" is a (sequence, row tile): `rows` consecutive query rows, row r of
+// a sequence being head r % G of its token r / G. A unit is a tile and a KV
+// head. The keys a tile needs are cut into chunks, and the chunks of all
+// units, in order (tile, KV head, chunk), are split evenly over the blocks of
+// one resident grid: block c of C takes [V c / C, V (c + 1) / C) of V. A unit
+// that lies in one block is finished there; each block leaves the partial
+// results of its first unit (begun in an earlier block) in slot 2 c and of its
+// last (continued in a later one) in slot 2 c + 1, as a normalised output and
+// log-sum-exp, and q8_merge_kernel joins them.
+#pragma once
+
+#include <climits>
+
+#include "ptx.cuh"
+#include "q8.cuh"
+
+namespace nsa {
+namespace q8 {
+
+enum { KEYS_ALL = NSA_KEYS_ALL, KEYS_WINDOW = NSA_KEYS_WINDOW, KEYS_BLOCKS = NSA_KEYS_BLOCKS };
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Tiles of sequence b, its first query row, queries and length. A length that
+// is out of range (or shorter than the queries) gives ok = false: its rows
+// have no keys.
+struct Seq {
+  int first, n, len;
+  bool ok;
+  unsigned err;  // its error-word bit when not ok
+};
+
+__device__ __forceinline__ Seq sequence(const Q8AttendArgs& a, int b) {
+  Seq s;
+  s.ok = token_range(a.cu, b, a.N, s.first, s.n);
+  s.err = s.ok ? 0u : kErrOffsets;
+  s.len = a.seq_lens[b];
+  // a single-token call takes an empty sequence; n queries need n tokens
+  if (s.len < 0 || s.len > a.T || (a.cu && s.len < s.n)) {
+    s.ok = false;
+    s.err |= kErrSeqLen;
+    s.len = 0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int tiles_of(const Q8AttendArgs& a, int n, int rows) {
+  return (int)(((long)n * a.G + rows - 1) / rows);
+}
+
+// Positions [lo, hi) of the keys that rows [r0, r0 + rows) of a sequence see
+// (their union). Rows of a bad sequence see none.
+__device__ __forceinline__ void key_span(const Q8AttendArgs& a, const Seq& s, int r0, int rows,
+                                         int& lo, int& hi) {
+  lo = hi = 0;
+  if (!s.ok || s.len == 0) return;
+  const int t0 = r0 / a.G;
+  const int t1 = min(s.n - 1, (r0 + rows - 1) / a.G);
+  const int at = s.len - s.n;  // position of the sequence's first query
+  hi = at + t1 + 1;
+  if (a.keys == KEYS_WINDOW) lo = max(0, at + t0 + 1 - a.window);
+}
+
+// Chunks of `chunk` keys that a tile needs; at least one, so that every row is written.
+__device__ __forceinline__ int chunks_of(const Q8AttendArgs& a, const Seq& s, int r0, int rows,
+                                         int chunk) {
+  if (a.keys == KEYS_BLOCKS) return (int)(((long)a.n * a.page + chunk - 1) / chunk);
+  int lo, hi;
+  key_span(a, s, r0, rows, lo, hi);
+  if (hi <= lo) return 1;
+  return (hi + chunk - 1) / chunk - lo / chunk;
+}
+
+// Block that holds position x of V positions split over C blocks: the largest
+// c with V c / C <= x.
+__device__ __forceinline__ int block_of(long x, long V, int C) {
+  int c = (int)((x * C + C - 1) / V);
+  if (c > C - 1) c = C - 1;
+  while (c > 0 && V * c / C > x) --c;
+  while (c < C - 1 && V * (c + 1) / C <= x) ++c;
+  return c;
+}
+
+// Per block: the unit of slot 2 c when that unit ends in the block (else -1),
+// and the block it begins in.
+struct MergeMeta {
+  long unit;
+  int from, pad;
+};
+
+}  // namespace q8
+}  // namespace nsa

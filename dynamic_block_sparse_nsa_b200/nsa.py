@@ -22,6 +22,9 @@ STATUS = {
     3: "NSA_ERR_WORKSPACE_TOO_SMALL", 4: "NSA_ERR_CUDA", 5: "NSA_ERR_DEVICE_TIMEOUT",
 }
 OP_COMPRESS, OP_PREFILL, OP_DECODE, OP_MOBA_PREFILL, OP_PREFILL_BACKWARD = 0, 1, 2, 3, 4
+OP_DECODE_Q8, OP_PREFILL_Q8 = 5, 6
+ROPE_STYLES = {"half": 0, "pairs": 1}
+KEYS = {"all": 0, "window": 1, "blocks": 2}
 DTYPE_F32, DTYPE_BF16 = 0, 1
 _TORCH_DTYPE = {DTYPE_F32: torch.float32, DTYPE_BF16: torch.bfloat16}
 
@@ -30,7 +33,8 @@ EXPORTS = (
     "nsa_workspace_size", "nsa_num_cmp_blocks", "nsa_compress_kv", "nsa_prefill",
     "nsa_prefill_backward", "nsa_decode",
     "moba_prefill", "nsa_decode_noalloc", "nsa_append_kv", "nsa_block_bounds",
-    "nsa_append_bounds", "nsa_decode_quest", "nsa_check", "nsa_debug_bounded_wait", "nsa_status_string",
+    "nsa_append_bounds", "nsa_decode_quest", "nsa_append_q8", "nsa_decode_q8", "nsa_prefill_q8",
+    "nsa_check", "nsa_debug_bounded_wait", "nsa_status_string",
     "nsa_last_error_detail", "nsa_trace_enable", "nsa_trace_set_filter", "nsa_trace_count",
     "nsa_trace_timed", "nsa_trace_get",
 )
@@ -57,6 +61,18 @@ class NsaParams(ctypes.Structure):
         return _TORCH_DTYPE[self.dtype]
 
 
+class NsaQ8Cache(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+    ]
+
+
+class NsaRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_int), ("dim", ctypes.c_int),
+                ("style", ctypes.c_int)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -77,6 +93,12 @@ def _load():
         "nsa_block_bounds": [P, vp, vp, vp, vp],
         "nsa_append_bounds": [P, vp, vp, vp, vp],
         "nsa_decode_quest": [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "nsa_append_q8": [P, ctypes.POINTER(NsaQ8Cache), vp, vp, ctypes.c_int, vp, vp,
+                          ctypes.POINTER(NsaRope), vp, vp, vp, vp, vp],
+        "nsa_decode_q8": [P, ctypes.POINTER(NsaQ8Cache), vp, vp, ctypes.c_int, vp, vp, vp, vp, sz,
+                          vp],
+        "nsa_prefill_q8": [P, ctypes.POINTER(NsaQ8Cache), vp, ctypes.c_int, vp, vp, ctypes.c_int,
+                           vp, vp, vp, sz, vp],
         "nsa_check": [vp],
         "nsa_debug_bounded_wait": [vp, ctypes.c_int, vp],
         "nsa_status_string": [ctypes.c_int],
@@ -394,6 +416,166 @@ def moba_prefill(p, q, k, v, out=None, sel_idx=None, ws=None, stream=None, want_
         _raise(LIB.moba_prefill(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
                                 _ptr(sel_idx), _ptr(ws), nbytes, _stream(stream, dev)))
     return out, sel_idx
+
+
+class Q8Cache:
+    """An 8-bit paged KV cache (include/nsa.h): k_pages, v_pages [P, Hkv, page, d]
+    float8_e4m3fn, k_scale, v_scale [P, Hkv] fp32, page_table [B, max_pages] int32.
+    The tensors are the caller's and may be written between calls."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table):
+        _dev(k_pages, "k_pages", torch.float8_e4m3fn)
+        dev = k_pages.device
+        _dev(v_pages, "v_pages", torch.float8_e4m3fn, dev)
+        _dev(k_scale, "k_scale", torch.float32, dev)
+        _dev(v_scale, "v_scale", torch.float32, dev)
+        _dev(page_table, "page_table", torch.int32, dev)
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must be [P, Hkv, page, d], of one shape")
+        if k_scale.shape != k_pages.shape[:2] or v_scale.shape != k_pages.shape[:2]:
+            raise ValueError("k_scale and v_scale must be [P, Hkv]")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [B, max_pages]")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.k_scale, self.v_scale, self.page_table = k_scale, v_scale, page_table
+        self.device = dev
+        self.c = NsaQ8Cache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                            v_scale.data_ptr(), page_table.data_ptr(), k_pages.shape[0])
+
+    def _fits(self, p):
+        if self.k_pages.shape[1:] != (p.Hkv, p.sel_block, p.d):
+            raise ValueError(f"pages are {tuple(self.k_pages.shape[1:])}, the parameters say "
+                             f"{(p.Hkv, p.sel_block, p.d)} (Hkv, sel_block, d)")
+        if self.page_table.shape != (p.B, -(-p.T // p.sel_block)):
+            raise ValueError(f"page_table is {tuple(self.page_table.shape)}, the parameters need "
+                             f"{(p.B, -(-p.T // p.sel_block))}")
+
+
+def q8_cache(p, num_pages, page_table):
+    """A Q8Cache of num_pages new pages (zero codes, scale 1) on page_table's device."""
+    dev = page_table.device
+    shape = (num_pages, p.Hkv, p.sel_block, p.d)
+
+    def pages():
+        return torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+
+    def scales():
+        return torch.ones(num_pages, p.Hkv, dtype=torch.float32, device=dev)
+
+    return Q8Cache(pages(), pages(), scales(), scales(), page_table)
+
+
+def rope_table(length, dim, base=10000.0, device="cuda"):
+    """The rotation table [length, 2, dim / 2] fp32 of angles t * base^(-2 i / dim),
+    the angles in fp64."""
+    freq = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.stack((angle.cos(), angle.sin()), dim=1).float().contiguous()
+
+
+def _shape(t, name, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def nsa_append_q8(p, k_new, v_new, pos, cache, cu_new=None, q=None, rope=None, rope_style="half",
+                  q_out=None, k_out=None, v_out=None, want_kv=False, stream=None):
+    """Append tokens k_new, v_new [N, Hkv, d] at positions pos[b] + i of the 8-bit
+    cache, keys (and q [N, Hq, d]) rotated by rope [len, 2, dim / 2] (see
+    rope_table). Returns (q_out, k_out, v_out): the rotated queries, and the
+    tokens as the cache holds them with want_kv (else None, unless given)."""
+    dt = p.torch_dtype
+    _dev(k_new, "k_new", dt, cache.device)
+    dev = cache.device
+    cache._fits(p)
+    N = k_new.shape[0]
+    kv, qs = (N, p.Hkv, p.d), (N, p.Hq, p.d)
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    if want_kv:
+        k_out = torch.empty_like(k_new) if k_out is None else k_out
+        v_out = torch.empty_like(k_new) if v_out is None else v_out
+    for t, nm, shape in ((k_new, "k_new", kv), (v_new, "v_new", kv), (q, "q", qs),
+                         (q_out, "q_out", qs), (k_out, "k_out", kv), (v_out, "v_out", kv)):
+        _dev(t, nm, dt, dev)
+        _shape(t, nm, shape)
+    _dev(pos, "pos", torch.int32, dev)
+    _shape(pos, "pos", (p.B,))
+    _dev(cu_new, "cu_new", torch.int32, dev)
+    _shape(cu_new, "cu_new", (p.B + 1,))
+    turn = None
+    if rope is not None:
+        _dev(rope, "rope", torch.float32, dev)
+        if rope.dim() != 3 or rope.shape[1] != 2:
+            raise ValueError(f"rope must be [len, 2, dim / 2], got {list(rope.shape)}")
+        if rope_style not in ROPE_STYLES:
+            raise ValueError(f"rope_style must be one of {sorted(ROPE_STYLES)}")
+        turn = ctypes.byref(NsaRope(rope.data_ptr(), rope.shape[0], 2 * rope.shape[2],
+                                    ROPE_STYLES[rope_style]))
+    with _on(dev):
+        _raise(LIB.nsa_append_q8(ctypes.byref(p), ctypes.byref(cache.c), _ptr(k_new), _ptr(v_new),
+                                 N, _ptr(pos), _ptr(cu_new), turn, _ptr(q), _ptr(q_out),
+                                 _ptr(k_out), _ptr(v_out), _stream(stream, dev)))
+    return q_out, k_out, v_out
+
+
+def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op):
+    """Checks of the attention arguments; allocates what is not given."""
+    dt, dev = p.torch_dtype, cache.device
+    cache._fits(p)
+    if keys not in KEYS:
+        raise ValueError(f"keys must be one of {sorted(KEYS)}")
+    shape = (N, p.Hq, p.d)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    for t, nm in ((q, "q"), (out, "out")):
+        _dev(t, nm, dt, dev)
+        _shape(t, nm, shape)
+    _dev(lse, "lse", torch.float32, dev)
+    _shape(lse, "lse", shape[:2])
+    _dev(seq_lens, "seq_lens", torch.int32, dev)
+    _shape(seq_lens, "seq_lens", (p.B,))
+    if ws is None:
+        ws = workspace(p, op, dev)
+    _dev(ws, "ws", None, dev)
+    return out, lse, ws, ws.numel() * ws.element_size()
+
+
+def nsa_decode_q8(p, q, cache, seq_lens, keys="all", sel_idx=None, out=None, lse=None, ws=None,
+                  stream=None):
+    """Attention of one query per sequence, q [B, Hq, d] at seq_lens[b] - 1, over the
+    8-bit cache: all keys, the last p.window, or those in the blocks sel_idx
+    [B, Hkv, p.top_n]. Returns (out, lse [B, Hq] fp32)."""
+    out, lse, ws, nbytes = _attend_q8_args(p, q, p.B, cache, seq_lens, keys, out, lse, ws,
+                                           OP_DECODE_Q8)
+    dev = cache.device
+    _dev(sel_idx, "sel_idx", torch.int32, dev)
+    _shape(sel_idx, "sel_idx", (p.B, p.Hkv, p.top_n))
+    with _on(dev):
+        _raise(LIB.nsa_decode_q8(ctypes.byref(p), ctypes.byref(cache.c), _ptr(q), _ptr(seq_lens),
+                                 KEYS[keys], _ptr(sel_idx), _ptr(out), _ptr(lse), _ptr(ws), nbytes,
+                                 _stream(stream, dev)))
+    return out, lse
+
+
+def nsa_prefill_q8(p, q, cache, seq_lens, cu_q=None, keys="all", out=None, lse=None, ws=None,
+                   stream=None):
+    """Causal attention of the queries q [N, Hq, d] (sequence b's at cu_q[b] ..
+    cu_q[b + 1] - 1, the last at position seq_lens[b] - 1) over the 8-bit cache:
+    all earlier keys or the last p.window. Returns (out, lse [N, Hq] fp32)."""
+    N = q.shape[0]
+    out, lse, ws, nbytes = _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws,
+                                           OP_PREFILL_Q8)
+    dev = cache.device
+    _dev(cu_q, "cu_q", torch.int32, dev)
+    _shape(cu_q, "cu_q", (p.B + 1,))
+    with _on(dev):
+        _raise(LIB.nsa_prefill_q8(ctypes.byref(p), ctypes.byref(cache.c), _ptr(q), N, _ptr(cu_q),
+                                  _ptr(seq_lens), KEYS[keys], _ptr(out), _ptr(lse), _ptr(ws),
+                                  nbytes, _stream(stream, dev)))
+    return out, lse
 
 
 def nsa_check(stream=None):

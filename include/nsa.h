@@ -25,7 +25,8 @@
  *     error nothing is written and a status other than NSA_OK is returned,
  *     with a message in nsa_last_error_detail().
  *   - Launch failures return NSA_ERR_CUDA. Faults found on the device (a
- *     bounded wait that gave up, a sequence length out of range) set a
+ *     bounded wait that gave up, a sequence length, append position, page
+ *     number or token offset out of range) set a
  *     per-device error word that nsa_check reports.
  *   - Thread safety: calls on different streams may run concurrently; the
  *     error-detail string is thread-local.
@@ -63,7 +64,9 @@ typedef enum {
   NSA_OP_PREFILL = 1,
   NSA_OP_DECODE = 2,
   NSA_OP_MOBA_PREFILL = 3,
-  NSA_OP_PREFILL_BACKWARD = 4
+  NSA_OP_PREFILL_BACKWARD = 4,
+  NSA_OP_DECODE_Q8 = 5,
+  NSA_OP_PREFILL_Q8 = 6
 } nsa_op;
 
 /* Problem description shared by all calls.
@@ -276,9 +279,131 @@ NSA_API nsa_status moba_prefill(const nsa_params* p, const void* q, const void* 
                         void* out, int32_t* sel_idx, void* workspace, size_t ws_bytes,
                         void* stream);
 
+/* ---- 8-bit paged KV cache ------------------------------------------------
+ *
+ * K and V in e4m3 codes (1 sign, 4 exponent, 3 mantissa bits; largest 448),
+ * in pages of sel_block tokens with one scale for each page and KV head: a
+ * component is code * scale. The page is the NSA selection block, so the block
+ * numbers that nsa_decode and nsa_decode_quest select address its pages. The
+ * sources describe no 8-bit or paged cache; it has no counterpart there.
+ *
+ *   k_pages, v_pages  [num_pages, Hkv, sel_block, d] e4m3 bytes, 16-byte
+ *              aligned (one head's page is contiguous).
+ *   k_scale, v_scale  [num_pages, Hkv] fp32, positive.
+ *   page_table [B, ceil(T / sel_block)] int32: token x of sequence b is slot
+ *              x % sel_block of page page_table[b, x / sel_block]. Entries of
+ *              pages that hold no live token are not used. Sequences may share
+ *              pages that none of them appends to.
+ * All in device memory. Of nsa_params the calls use B, T (tokens a sequence
+ * can have), Hq, Hkv, d, sel_block (16, 32, 64 or 128), dtype (of q, k, v and
+ * outputs) and, for attention, softmax_scale, window and top_n. */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int num_pages;
+} nsa_q8_cache;
+
+/* Position rotation of the first `dim` components x of a key or query at
+ * position t: for each of the dim / 2 pairs i, (x_a, x_b) becomes
+ * (x_a cos - x_b sin, x_b cos + x_a sin) with cos = table[t, 0, i], sin =
+ * table[t, 1, i]. NSA_ROPE_HALF: a = i, b = i + dim / 2. NSA_ROPE_PAIRS:
+ * a = 2 i, b = 2 i + 1. Computed in fp32.
+ *   table      [len, 2, dim / 2] fp32, device, 16-byte aligned.
+ *   dim        a multiple of 16, at most d. */
+typedef enum { NSA_ROPE_HALF = 0, NSA_ROPE_PAIRS = 1 } nsa_rope_style;
+typedef struct {
+  const float* table;
+  int len;
+  int dim;
+  int style;
+} nsa_rope;
+
+/* Appends new tokens to the 8-bit cache; keys are rotated by their position on
+ * the way, and so are the queries of the same tokens.
+ *   k_new, v_new  [N, Hkv, d] dtype.
+ *   pos        [B] int32, device: the sequence's length before the append; its
+ *              i-th new token is written at position pos[b] + i.
+ *   cu_new     [B + 1] int32, device, ascending, or NULL: the new tokens of
+ *              sequence b are rows cu_new[b] .. cu_new[b + 1] - 1 (none is
+ *              fine); rows outside are ignored. NULL: one token per sequence,
+ *              row b (N == B).
+ *   rope       NULL: no rotation.
+ *   q, q_out   [N, Hq, d] dtype, or both NULL: the rotated queries (q_out == q
+ *              is allowed).
+ *   k_out, v_out  [N, Hkv, d] dtype, or both NULL: the new tokens as the cache
+ *              holds them (rotated, quantised), rounded to dtype.
+ * Per (page, head) of K and of V: with a the largest finite magnitude the call
+ * writes there, need = the smallest power of two >= 2^-126 with a <= 448 need.
+ * The scale becomes need when the call writes the page's first slot, else
+ * max(scale, need). When it changes, the codes of the page's other slots are
+ * re-coded so that they stand for the same values (exact but for those that
+ * fall below e4m3's normal range; in a page that the call begins, values of
+ * stale slots beyond the new range become NaN). A component's code is
+ * x / scale rounded once from the fp32 x, to nearest even; NaN and infinities
+ * become NaN. So a page filled by several calls holds what one call's scale
+ * gives, up to the re-coded small values.
+ *   A sequence whose positions leave [0, T) or the rotation table is not
+ *   written (device error word; nsa_check: NSA_ERR_INVALID_ARGUMENT); so are a
+ *   page whose number is outside [0, num_pages) and a sequence whose offsets
+ *   are out of order. Two sequences must not append to one page. */
+NSA_API nsa_status nsa_append_q8(const nsa_params* p, const nsa_q8_cache* cache,
+                                 const void* k_new, const void* v_new, int N, const int32_t* pos,
+                                 const int32_t* cu_new, const nsa_rope* rope, const void* q,
+                                 void* q_out, void* k_out, void* v_out, void* stream);
+
+/* Keys that a query at position t of its sequence attends to, of [0, t]:
+ * NSA_KEYS_ALL: all; NSA_KEYS_WINDOW: the last `window` (its own included);
+ * NSA_KEYS_BLOCKS (nsa_decode_q8): those in the listed blocks. */
+typedef enum { NSA_KEYS_ALL = 0, NSA_KEYS_WINDOW = 1, NSA_KEYS_BLOCKS = 2 } nsa_keys;
+
+/* Single-token attention over the 8-bit cache: softmax(scale q . k) v of one
+ * query per sequence over its keys, out of HBM bytes: the codes are read once.
+ *   q          [B, Hq, d] dtype: the query at position seq_lens[b] - 1.
+ *   seq_lens   [B] int32, device, 0 <= seq_lens[b] <= T (0: no keys).
+ *   keys       nsa_keys.
+ *   sel_idx    [B, Hkv, top_n] int32 (NSA_KEYS_BLOCKS; else ignored): block
+ *              numbers as nsa_decode writes them, in any order; negative
+ *              entries and those at or past the length are ignored, a repeated
+ *              one counts once.
+ *   out        [B, Hq, d] dtype.
+ *   lse        [B, Hq] fp32 or NULL: natural logarithm of the sum of
+ *              exp(scale q . k), to join with other branches' outputs.
+ * A query without keys gives 0 and -inf. A length outside [0, T] does too and
+ * sets the device error word; the tokens of a page whose number is outside
+ * [0, num_pages) are left out, and set it. NaN components of keys and values
+ * reach the queries that attend to them and no others.
+ *   workspace  nsa_workspace_size(NSA_OP_DECODE_Q8) bytes; calls that may
+ *              overlap on the GPU need one each. */
+NSA_API nsa_status nsa_decode_q8(const nsa_params* p, const nsa_q8_cache* cache, const void* q,
+                                 const int32_t* seq_lens, int keys, const int32_t* sel_idx,
+                                 void* out, float* lse, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/* Causal attention of chunks of queries over the 8-bit cache, which already
+ * holds the chunks' own keys and values (chunked prompts, draft tokens).
+ *   q          [N, Hq, d] dtype, N <= B * T.
+ *   cu_q       [B + 1] int32, device, ascending, or NULL (one query per
+ *              sequence, N == B): sequence b's n queries are rows cu_q[b] ..
+ *              cu_q[b + 1] - 1, the i-th at position seq_lens[b] - n + i.
+ *              Rows outside are not written.
+ *   seq_lens   [B] int32, device: tokens in the cache, n <= seq_lens[b] <= T.
+ *   keys       NSA_KEYS_ALL or NSA_KEYS_WINDOW.
+ *   out, lse   [N, Hq, d] dtype, [N, Hq] fp32 or NULL.
+ *   workspace  nsa_workspace_size(NSA_OP_PREFILL_Q8) bytes.
+ * Errors and NaN as nsa_decode_q8; a sequence whose offsets are out of order
+ * is not written. */
+NSA_API nsa_status nsa_prefill_q8(const nsa_params* p, const nsa_q8_cache* cache, const void* q,
+                                  int N, const int32_t* cu_q, const int32_t* seq_lens, int keys,
+                                  void* out, float* lse, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
 /* Synchronise `stream`, then read and clear this device's error word:
  * NSA_ERR_DEVICE_TIMEOUT if a bounded wait gave up, NSA_ERR_INVALID_ARGUMENT
- * if a kernel met an out-of-range sequence length, else NSA_OK (or
+ * if a kernel met an out-of-range sequence length, append position, page
+ * number or token offset, else NSA_OK (or
  * NSA_ERR_CUDA if the synchronisation itself failed). */
 NSA_API nsa_status nsa_check(void* stream);
 

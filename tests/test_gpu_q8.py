@@ -1,0 +1,611 @@
+"""The 8-bit paged cache on the GPU against the 64-bit definitions of
+tests/q8_ref.py: append with rotation, single-token attention, chunks, and a
+serving loop of them together."""
+import math
+
+import pytest
+import torch
+
+from tests import q8_ref as ref
+
+pytestmark = pytest.mark.gpu
+nsa = pytest.importorskip("dynamic_block_sparse_nsa_b200.nsa")
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word(cuda_ok):
+    yield
+    nsa.nsa_check()  # no test leaves a device error behind
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def random_cache(p, lens, seed, extra=3, spread=1.0):
+    """A cache whose sequences' pages lie scattered in the pool; slots that no
+    token lives in hold arbitrary codes, the NaN code among them."""
+    g = gen(seed)
+    wide = -(-p.T // p.sel_block)
+    count = [-(-n // p.sel_block) for n in lens]
+    P = sum(count) + extra
+    order = torch.randperm(P, generator=g).to(torch.int32)
+    table = torch.full((p.B, wide), -1, dtype=torch.int32)  # unused entries are no pages
+    at = 0
+    for b, c in enumerate(count):
+        table[b, :c] = order[at:at + c]
+        at += c
+
+    def pool():
+        x = torch.randn(P, p.Hkv, p.sel_block, p.d, generator=g)
+        s = torch.exp2(torch.randint(-2, 3, (P, p.Hkv), generator=g).float() * spread - 5)
+        s *= 1 + torch.rand(P, p.Hkv, generator=g)  # attention takes any positive scale
+        codes = (x / s[..., None, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        dead = torch.ones(P, p.sel_block, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for j in range(count[b]):
+                dead[table[b, j], :max(0, min(p.sel_block, n - j * p.sel_block))] = False
+        noise = torch.randint(0, 256, codes.shape, generator=g, dtype=torch.uint8)
+        noise[..., ::3] = 0x7f
+        codes = torch.where(dead[:, None, :, None], noise, codes)
+        return codes.view(torch.float8_e4m3fn).cuda(), s.cuda()
+
+    k, ks = pool()
+    v, vs = pool()
+    return nsa.Q8Cache(k, v, ks, vs, table.cuda())
+
+
+def check_attention(got, p, q, cache, lens, cu=None, keys="all", sel=None, scale=None):
+    out, lse = got
+    want, wlse, A, B = ref.attend(q, cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+                                  cache.page_table, lens, p.sel_block, cu, keys, p.window, sel,
+                                  scale)
+    t_out, t_lse = ref.bounds(want, wlse, A, B, p.torch_dtype, max(1, int(lens.max())))
+    rows = torch.isfinite(want).all(-1).all(-1)
+    out, lse = out.double().cpu(), lse.double().cpu()
+    err = (out - want).abs()
+    assert (err <= t_out)[rows].all(), (float((err / t_out)[rows].max()), float(err[rows].max()))
+    empty = torch.isinf(wlse) & rows[:, None]
+    assert (lse[empty] == -math.inf).all()
+    fine = ~empty & rows[:, None]
+    assert ((lse - wlse).abs() <= t_lse)[fine].all(), float(((lse - wlse).abs() / t_lse)[fine].max())
+
+
+# ---- append -----------------------------------------------------------------
+
+def check_append(p, cache, k, v, pos, cu, rope, style, q=None, steps=1):
+    before = [t.clone() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+    want = ref.append(k, v, pos.cpu(), None if cu is None else cu.cpu(), before[:2], before[2:],
+                      cache.page_table, p.sel_block, rope, style)
+    q_out, k_out, v_out = nsa.nsa_append_q8(p, k, v, pos, cache, cu_new=cu, q=q, rope=rope,
+                                            rope_style=style, want_kv=True)
+    nsa.nsa_check()
+    table = cache.page_table.cpu()
+    for (name, codes, scale, x, slack), pages, sc, held in zip(
+            want, (cache.k_pages, cache.v_pages), (cache.k_scale, cache.v_scale), (k_out, v_out)):
+        got, gs = ref.decode(pages), sc.cpu().double()
+        if name == "v" or rope is None:  # nothing is computed before the codes
+            assert torch.equal(got.nan_to_num(nan=999.0), codes.nan_to_num(nan=999.0)), name
+            assert torch.equal(gs, scale), name
+        for b in range(p.B):
+            lo, hi = ref.tokens(cu, b)
+            for r in range(lo, hi):
+                t = int(pos[b]) + r - lo
+                pid, slot = int(table[b, t // p.sel_block]), t % p.sel_block
+                s = gs[pid][:, None]
+                stored = got[pid, :, slot]
+                fine = torch.isfinite(x[r])
+                assert torch.equal(torch.isnan(stored), ~fine), name
+                err = (stored * s - x[r]).abs()[fine]
+                half = (ref.step_of(stored.nan_to_num()) / 2 * s)[fine]
+                assert (err <= half * (1 + 2.0 ** -20) + slack[r][fine]).all(), name
+                # the rows as held, rounded to dtype (exact in both: 4 significant bits)
+                assert torch.equal(held[r].cpu().double().nan_to_num(nan=999.0),
+                                   (stored * s).nan_to_num(nan=999.0)), name
+        if name == "k" and rope is not None:
+            # a scale may differ where the rotated maximum lies on a power of two
+            same = gs == scale
+            assert ((gs == scale) | (gs == 2 * scale) | (2 * gs == scale)).all()
+            assert same.double().mean() > 0.99 or same.numel() < 100
+    if q is not None and rope is not None:
+        for b in range(p.B):
+            lo, hi = ref.tokens(cu, b)
+            if hi == lo:
+                continue
+            at = torch.arange(int(pos[b]), int(pos[b]) + hi - lo)
+            x = q[lo:hi].cpu().double()
+            y = ref.turned(x, rope, at, style)
+            lim = 2.0 ** -21 * (x.abs().amax(-1, keepdim=True) * 2)
+            lim = lim + y.abs() * (2.0 ** -8 if p.torch_dtype == BF16 else 2.0 ** -24)
+            assert ((q_out[lo:hi].cpu().double() - y).abs() <= lim).all()
+    return q_out, k_out, v_out
+
+
+APPENDS = [
+    # B, Hq, Hkv, d, page, dtype, rot, style, past, new
+    (1, 4, 1, 128, 64, BF16, 128, "half", [0], [1]),
+    (1, 4, 2, 128, 64, BF16, 128, "half", [0], [200]),
+    (3, 6, 3, 64, 16, F32, 32, "pairs", [5, 0, 47], [40, 1, 17]),
+    (2, 5, 5, 128, 32, BF16, 64, "pairs", [31, 64], [2, 65]),
+    (4, 8, 1, 128, 128, F32, 128, "half", [100, 0, 127, 1], [0, 300, 2, 1]),
+    (2, 2, 2, 64, 64, BF16, 16, "half", [63, 3], [129, 61]),
+    (2, 7, 1, 64, 128, BF16, 64, "half", [0, 200], [128, 57]),
+    (2, 3, 3, 64, 32, F32, 48, "pairs", [1, 0], [31, 32]),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS, ids=lambda c: f"B{c[0]}_d{c[3]}_page{c[4]}_{c[7]}")
+@pytest.mark.parametrize("big", (1.0, 300.0))
+def test_append_matches_the_definition(case, big):
+    """Chunks into new and part-filled pages, whose scales stay (big = 1) or grow."""
+    B, Hq, Hkv, d, page, dt, rot, style, past, new = case
+    T = max(a + n for a, n in zip(past, new))
+    p = nsa.params(B, T, Hq, Hkv, d, sel_block=page, dtype=dt)
+    cache = random_cache(p, [a + n for a, n in zip(past, new)], 1, spread=2.0)
+    # a part-filled page's scale is a power of two in a cache that appends wrote
+    for sc in (cache.k_scale, cache.v_scale):
+        sc.copy_(torch.exp2(torch.floor(torch.log2(sc))))
+    g = gen(2)
+    N = sum(new)
+    k = (torch.randn(N, Hkv, d, generator=g) * big).to(dt).cuda()
+    v = (torch.randn(N, Hkv, d, generator=g) * big).to(dt).cuda()
+    q = torch.randn(N, Hq, d, generator=g).to(dt).cuda()
+    cu = i32([0] + torch.tensor(new).cumsum(0).tolist())
+    check_append(p, cache, k, v, i32(past), cu, nsa.rope_table(T, rot), style, q)
+
+
+@pytest.mark.parametrize("dt", (BF16, F32))
+@pytest.mark.parametrize("d,page,style", ((128, 64, "half"), (64, 16, "pairs")))
+def test_append_one_token_per_sequence(dt, d, page, style):
+    past = [0, 1, page - 1, page, 3 * page + 7]
+    T = 5 * page
+    p = nsa.params(5, T, 12, 3, d, sel_block=page, dtype=dt)
+    cache = random_cache(p, [a + 1 for a in past], 3)
+    for sc in (cache.k_scale, cache.v_scale):
+        sc.copy_(torch.exp2(torch.floor(torch.log2(sc))))
+    g = gen(4)
+    make = lambda h: torch.randn(5, h, d, generator=g).to(dt).cuda()  # noqa: E731
+    k, v, q = make(3) * 50, make(3) * 0.01, make(12)
+    check_append(p, cache, k, v, i32(past), None, nsa.rope_table(T, d), style, q)
+    # the same through offsets
+    again = random_cache(p, [a + 1 for a in past], 3)
+    for sc in (again.k_scale, again.v_scale):
+        sc.copy_(torch.exp2(torch.floor(torch.log2(sc))))
+    nsa.nsa_append_q8(p, k, v, i32(past), again, cu_new=i32(list(range(6))),
+                      rope=nsa.rope_table(T, d), rope_style=style)
+    for a, b in ((cache.k_pages, again.k_pages), (cache.v_pages, again.v_pages)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(cache.k_scale, again.k_scale) and torch.equal(cache.v_scale, again.v_scale)
+
+
+def test_append_without_rotation_zero_and_non_finite():
+    """No rotation: codes are exact. A head of zeros takes the smallest scale;
+    NaN and infinities become NaN and do not set the scale; the largest and
+    smallest magnitudes stay in range."""
+    p = nsa.params(1, 64, 2, 2, 64, sel_block=16, dtype=F32)
+    cache = random_cache(p, [64], 5)
+    k = torch.randn(40, 2, 64, generator=gen(6))
+    k[:16, 0] = 0.0
+    k[3, 1, 5], k[4, 1, 6], k[5, 1, 7] = math.nan, math.inf, -math.inf
+    k[17, 0, 0] = 3.0e38
+    k[32:, 0] *= 1e-38
+    k[33:, 1] = math.nan
+    v = k.flip(0).contiguous()
+    check_append(p, cache, k.cuda(), v.cuda(), i32([0]), i32([0, 40]), None, "half")
+
+
+def test_append_token_by_token_equals_one_call():
+    """Values of equal magnitude: a page grown token by token holds what one
+    call writes; and calls repeat bit for bit."""
+    p = nsa.params(1, 256, 4, 2, 128, sel_block=64)
+    sign = torch.randint(0, 2, (150, 2, 128), generator=gen(7)).float() * 2 - 1
+    k = (sign * torch.exp2(torch.randint(-3, 1, (150, 2, 128), generator=gen(8)).float())).to(BF16)
+    k[..., 0] = 1.0  # every token's largest magnitude
+    k = k.cuda()
+    table = i32([[2, 0, 3, 1]])
+    one, steps = nsa.q8_cache(p, 4, table), nsa.q8_cache(p, 4, table)
+    nsa.nsa_append_q8(p, k, k, i32([0]), one, cu_new=i32([0, 150]))
+    for t in range(150):
+        nsa.nsa_append_q8(p, k[t:t + 1], k[t:t + 1], i32([t]), steps)
+    live = [(2, 64), (0, 64), (3, 22)]
+    for a, b in ((one.k_pages, steps.k_pages), (one.v_pages, steps.v_pages)):
+        for pid, n in live:
+            assert torch.equal(a.view(torch.uint8)[pid, :, :n], b.view(torch.uint8)[pid, :, :n])
+    assert torch.equal(one.k_scale, steps.k_scale)
+
+
+def test_append_padded_rows_and_other_pages_stay():
+    """Rows behind the last sequence are ignored; pages of no new token keep
+    their bytes; q_out may be q."""
+    p = nsa.params(2, 100, 4, 1, 64, sel_block=32, dtype=BF16)
+    cache = random_cache(p, [100, 70], 9)
+    before = [t.clone() for t in (cache.k_pages, cache.v_pages, cache.k_scale)]
+    k = (torch.randn(20, 1, 64, generator=gen(10)) * 1e-3).to(BF16).cuda()  # no scale grows
+    q = torch.randn(20, 4, 64, generator=gen(11)).to(BF16).cuda()
+    keep = q.clone()
+    cu = i32([0, 9, 12])
+    q_out, k_out, _ = nsa.nsa_append_q8(p, k, k, i32([60, 33]), cache, cu_new=cu, q=q, q_out=q,
+                                        rope=nsa.rope_table(100, 64), want_kv=True)
+    nsa.nsa_check()
+    assert q_out is q and torch.equal(q[12:], keep[12:]) and not torch.equal(q[:12], keep[:12])
+    touched = {int(cache.page_table[0, 1]), int(cache.page_table[0, 2]), int(cache.page_table[1, 1])}
+    for pid in set(range(before[0].shape[0])) - touched:
+        assert torch.equal(cache.k_pages.view(torch.uint8)[pid], before[0].view(torch.uint8)[pid])
+        assert torch.equal(cache.v_pages.view(torch.uint8)[pid], before[1].view(torch.uint8)[pid])
+    later = cache.page_table[1, 1]  # sequence 1 wrote slots 1 .. 3 of it
+    if torch.equal(cache.k_scale[later], before[2][later]):
+        assert torch.equal(cache.k_pages.view(torch.uint8)[later, :, 4:],
+                           before[0].view(torch.uint8)[later, :, 4:])
+
+
+def test_append_reports_bad_positions_pages_and_offsets():
+    p = nsa.params(3, 64, 2, 1, 64, sel_block=16, dtype=F32)
+    rope = nsa.rope_table(32, 64)
+    k = torch.randn(6, 1, 64, generator=gen(12)).cuda()
+
+    def refused(pos, cu, table=None, turn=None):
+        cache = nsa.q8_cache(p, 4, i32([[0, 1, 2, 3]] * 3) if table is None else table)
+        nsa.nsa_append_q8(p, k if cu is not None else k[:3], k if cu is not None else k[:3],
+                          i32(pos), cache, cu_new=None if cu is None else i32(cu), rope=turn)
+        with pytest.raises(nsa.NsaError) as e:
+            nsa.nsa_check()
+        assert e.value.status == 1
+        return cache, str(e.value)
+
+    cache, text = refused([-1, 64, 70], None)
+    assert "position" in text and not cache.k_pages.view(torch.uint8).any()
+    cache, text = refused([63, -5, 40], [0, 2, 4, 6], turn=rope)  # 40 is past the table of 32
+    assert "position" in text and not cache.k_pages.view(torch.uint8).any()
+    cache, text = refused([0, 0, 0], [0, 9, 4, 2])
+    assert "offsets" in text
+    cache, text = refused([0, 0, 0], None, table=i32([[-1, 0, 0, 0], [4, 0, 0, 0], [99, 0, 0, 0]]))
+    assert "page" in text and not cache.k_pages.view(torch.uint8).any()
+
+
+# ---- attention: single tokens ---------------------------------------------------
+
+DECODES = [
+    # Hq, Hkv, d, page, dtype, lens
+    (16, 1, 128, 64, BF16, [1, 2, 31, 32, 33, 63, 64, 65, 0, 500]),
+    (64, 4, 128, 64, BF16, [1000, 3, 700]),
+    (8, 8, 128, 128, BF16, [129, 700]),
+    (40, 8, 64, 16, F32, [333, 0, 17, 1, 16]),
+    (6, 2, 128, 32, F32, [257, 31]),
+    (20, 1, 64, 64, BF16, [130, 5]),        # more than 16 heads to a KV head
+    (34, 2, 128, 16, F32, [77, 48]),
+    (5, 1, 64, 128, F32, [400]),
+    (4, 4, 64, 32, BF16, [90, 1, 64]),
+]
+
+
+@pytest.mark.parametrize("case", DECODES, ids=lambda c: f"h{c[0]}_{c[1]}_d{c[2]}_page{c[3]}")
+@pytest.mark.parametrize("keys", ("all", "window", "blocks"))
+def test_decode_matches_the_definition(case, keys):
+    Hq, Hkv, d, page, dt, lens = case
+    B, T = len(lens), max(lens) + 5
+    g = gen(20)
+    for window, n in ((1, 1), (37, 3), (64, 9), (10000, 40)) if keys != "all" else ((1, 1),):
+        p = nsa.params(B, T, Hq, Hkv, d, sel_block=page, dtype=dt, window=window, top_n=n)
+        cache = random_cache(p, lens, 21)
+        q = torch.randn(B, Hq, d, generator=g).to(dt).cuda()
+        sel = None
+        if keys == "blocks":  # any order, repeated, negative and past the end
+            sel = torch.randint(-2, -(-T // page) + 2, (B, Hkv, n), generator=g).to(torch.int32)
+        got = nsa.nsa_decode_q8(p, q, cache, i32(lens), keys=keys,
+                                sel_idx=None if sel is None else sel.cuda())
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, i32(lens), None, keys, sel)
+
+
+def test_decode_many_sequences_and_long_ones():
+    """Units that span blocks, warps and both; more tiles than a block plans."""
+    for B, Hq, Hkv, lens in ((1, 16, 1, [20000]), (1200, 2, 1, None), (37, 8, 2, None)):
+        if lens is None:
+            lens = torch.randint(0, 90, (B,), generator=gen(22)).tolist()
+        p = nsa.params(B, max(lens), Hq, Hkv, 128, sel_block=64)
+        cache = random_cache(p, lens, 23)
+        q = torch.randn(B, Hq, 128, generator=gen(24)).to(BF16).cuda()
+        got = nsa.nsa_decode_q8(p, q, cache, i32(lens))
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, i32(lens))
+
+
+def test_decode_scales_far_apart():
+    """Pages whose value scales differ by up to 2^200, with the large ones hardly
+    attended: their products leave fp16's and fp32's ranges on the way."""
+    p = nsa.params(1, 256, 4, 1, 64, sel_block=64, dtype=F32)
+    for big, order in ((2.0 ** 90, [0, 1, 2, 3]), (2.0 ** 90, [3, 2, 1, 0]), (2.0 ** 20, [1, 3, 0, 2])):
+        cache = random_cache(p, [256], 25, extra=0)
+        k = torch.full((4, 1, 64, 64), 1.0)
+        k[1] = -1.0                                   # page 1: scores far below the others'
+        cache.k_pages.copy_(k.to(torch.float8_e4m3fn))
+        cache.k_scale.fill_(1.0)
+        cache.v_scale.copy_(torch.tensor([[1.0], [big], [2.0 ** -100], [2.0 ** -126]]))
+        cache.page_table.copy_(i32([order]))
+        q = torch.full((1, 4, 64), 6.0).cuda()        # e^(-96): 2^-138 of the others
+        got = nsa.nsa_decode_q8(p, q, cache, i32([256]))
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, i32([256]))
+
+
+def test_decode_softmax_scale_and_extreme_scores():
+    p = nsa.params(2, 100, 8, 2, 64, sel_block=32, dtype=F32, softmax_scale=0.5)
+    cache = random_cache(p, [100, 50], 26)
+    q = torch.randn(2, 8, 64, generator=gen(27))
+    q[0] *= 1e-3
+    q[1] *= 4.0
+    got = nsa.nsa_decode_q8(p, q.cuda(), cache, i32([100, 50]))
+    check_attention(got, p, q, cache, i32([100, 50]), scale=0.5)
+    q[0], q[1] = 1e30, 0.0  # finite scores beyond any exponent: the largest key wins
+    cache.k_scale.fill_(1.0)
+    out, lse = nsa.nsa_decode_q8(p, q.cuda(), cache, i32([100, 50]))
+    nsa.nsa_check()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+def test_decode_non_finite_components():
+    """A NaN key or value reaches the queries that attend to it and no others."""
+    p = nsa.params(2, 128, 4, 2, 64, sel_block=32, dtype=BF16, window=40, top_n=1)
+    cache = random_cache(p, [128, 128], 28)
+    q = torch.randn(2, 4, 64, generator=gen(29)).to(BF16).cuda()
+    base = nsa.nsa_decode_q8(p, q, cache, i32([128, 128]), keys="window")[0]
+    pid = int(cache.page_table[0, 2])  # positions 64 .. 95: 88 on are in the window
+    cache.k_pages.view(torch.uint8)[pid, 0, 10] = 0x7f
+    cache.v_pages.view(torch.uint8)[pid, 1, 23, 7] = 0xff
+    out = nsa.nsa_decode_q8(p, q, cache, i32([128, 128]), keys="window")[0]
+    assert torch.equal(out, base)
+    cache.v_pages.view(torch.uint8)[pid, 1, 24, 7] = 0xff
+    out = nsa.nsa_decode_q8(p, q, cache, i32([128, 128]), keys="window")[0]
+    bad = torch.isnan(out)
+    assert bad[0, 2:, 7].all() and int(bad.sum()) == 2
+    cache.k_pages.view(torch.uint8)[pid, 0, 30] = 0x7f
+    out, lse = nsa.nsa_decode_q8(p, q, cache, i32([128, 128]), keys="window")
+    assert torch.isnan(out[0, :2]).all() and torch.isnan(lse[0, :2]).all()
+    assert torch.isfinite(out[1]).all()
+    qn = q.clone()
+    qn[1, 0, 0] = math.nan
+    qn[1, 1, 0] = math.inf
+    out = nsa.nsa_decode_q8(p, qn, cache, i32([128, 128]))[0]
+    assert torch.isnan(out[1, 0]).all() and torch.isfinite(out[1, 2:]).all()
+
+
+def test_attention_reports_bad_lengths_pages_and_offsets():
+    p = nsa.params(3, 128, 4, 1, 64, sel_block=32, dtype=BF16)
+    cache = random_cache(p, [128, 100, 64], 30)
+    q = torch.randn(3, 4, 64, generator=gen(31)).to(BF16).cuda()
+    out, lse = nsa.nsa_decode_q8(p, q, cache, i32([128, 129, -1]))
+    with pytest.raises(nsa.NsaError, match="length"):
+        nsa.nsa_check()
+    assert not out[1:].any() and (lse[1:] == -math.inf).all() and torch.isfinite(out[0]).all()
+    check_attention((out[:1], lse[:1]), nsa.params(1, 128, 4, 1, 64, sel_block=32), q[:1],
+                    nsa.Q8Cache(cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+                                cache.page_table[:1].contiguous()), i32([128]))
+    # pages outside the pool are left out
+    cache.page_table[0, 1] = 9999
+    cache.page_table[1, 0] = -3
+    got = nsa.nsa_decode_q8(p, q, cache, i32([128, 100, 64]))
+    with pytest.raises(nsa.NsaError, match="page"):
+        nsa.nsa_check()
+    check_attention(got, p, q, cache, i32([128, 100, 64]))
+    # offsets past the rows: that sequence is not written; more queries than tokens: zeros
+    cache = random_cache(p, [128, 100, 64], 30)
+    q = torch.randn(12, 4, 64, generator=gen(32)).to(BF16).cuda()
+    out = torch.full_like(q, 7.0)
+    cu = i32([0, 4, 6, 40])
+    _, lse = nsa.nsa_prefill_q8(p, q, cache, i32([128, 1, 64]), cu, out=out)
+    with pytest.raises(nsa.NsaError, match="length"):
+        nsa.nsa_check()
+    assert not out[4:6].any() and (lse[4:6] == -math.inf).all() and (out[6:] == 7.0).all()
+    assert torch.isfinite(out[:4]).all() and not (out[:4] == 7.0).all(-1).any()
+    nsa.nsa_prefill_q8(p, q, cache, i32([128, 100, 64]), cu)
+    with pytest.raises(nsa.NsaError, match="offsets"):
+        nsa.nsa_check()
+
+
+# ---- attention: chunks ------------------------------------------------------------
+
+PREFILLS = [
+    # Hq, Hkv, d, page, dtype, lens, new
+    (16, 1, 128, 64, BF16, [70], [70]),
+    (64, 4, 128, 64, BF16, [300, 129], [130, 5]),
+    (8, 2, 128, 128, BF16, [257, 1, 40], [100, 1, 0]),
+    (10, 2, 64, 16, F32, [60, 33], [33, 33]),
+    (6, 6, 128, 32, F32, [64, 90], [20, 3]),
+    (20, 1, 64, 64, BF16, [77], [9]),
+    (32, 8, 128, 16, BF16, [150, 17], [80, 17]),
+    (7, 1, 128, 32, BF16, [200], [61]),
+    (4, 1, 64, 128, F32, [131], [131]),
+]
+
+
+@pytest.mark.parametrize("case", PREFILLS, ids=lambda c: f"h{c[0]}_{c[1]}_d{c[2]}_page{c[3]}")
+@pytest.mark.parametrize("keys", ("all", "window"))
+def test_prefill_matches_the_definition(case, keys):
+    Hq, Hkv, d, page, dt, lens, new = case
+    N = sum(new) + 3  # rows behind the last sequence
+    for window in (1, 20, 64) if keys == "window" else (1,):
+        p = nsa.params(len(lens), max(lens) + 20, Hq, Hkv, d, sel_block=page, dtype=dt,
+                       window=window)
+        cache = random_cache(p, lens, 40)
+        q = torch.randn(N, Hq, d, generator=gen(41)).to(dt).cuda()
+        cu = i32([0] + torch.tensor(new).cumsum(0).tolist())
+        out = torch.full_like(q, 5.0)
+        lse = torch.full((N, Hq), 5.0, device="cuda")
+        nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu, keys=keys, out=out, lse=lse)
+        nsa.nsa_check()
+        assert (out[-3:] == 5.0).all() and (lse[-3:] == 5.0).all()
+        check_attention((out, lse), p, q, cache, i32(lens), cu.cpu(), keys)
+
+
+def test_prefill_rows_equal_single_tokens():
+    """A chunk's rows agree with the same queries one at a time (fp32)."""
+    p = nsa.params(1, 90, 6, 2, 128, sel_block=32, dtype=F32)
+    cache = random_cache(p, [90], 42)
+    q = torch.randn(12, 6, 128, generator=gen(43)).cuda()
+    out, lse = nsa.nsa_prefill_q8(p, q, cache, i32([90]), i32([0, 12]))
+    for i in range(12):
+        o, s = nsa.nsa_decode_q8(p, q[i:i + 1], cache, i32([79 + i]))
+        torch.testing.assert_close(o[0], out[i], rtol=2e-5, atol=2e-5)
+        torch.testing.assert_close(s[0], lse[i], rtol=2e-5, atol=2e-5)
+
+
+@pytest.mark.parametrize("dt,d,Hq", ((BF16, 128, 16), (F32, 64, 4), (BF16, 128, 2)))
+def test_prefill_nan_values_reach_later_queries_only(dt, d, Hq):
+    p = nsa.params(1, 200, Hq, 1, d, sel_block=64, dtype=dt, window=30)
+    for keys in ("all", "window"):
+        cache = random_cache(p, [200], 44)
+        q = torch.randn(100, Hq, d, generator=gen(45)).to(dt).cuda()
+        base = nsa.nsa_prefill_q8(p, q, cache, i32([200]), i32([0, 100]), keys=keys)[0]
+        for pos, dim in ((150, 3), (161, 3), (128, d - 1)):
+            pid = int(cache.page_table[0, pos // 64])
+            cache.v_pages.view(torch.uint8)[pid, 0, pos % 64, dim] = 0x7f
+        pid = int(cache.page_table[0, 190 // 64])
+        cache.k_pages.view(torch.uint8)[pid, 0, 190 % 64, 0] = 0x7f
+        out = nsa.nsa_prefill_q8(p, q, cache, i32([200]), i32([0, 100]), keys=keys)[0]
+        nsa.nsa_check()
+        t = 100 + torch.arange(100)
+        last = 200 if keys == "all" else 30
+        sees = lambda x: (t >= x) & (t < x + last)  # noqa: E731
+        want = torch.zeros(100, Hq, d, dtype=torch.bool)
+        want[sees(150) | sees(161), :, 3] = True
+        want[sees(128), :, d - 1] = True
+        want[sees(190)] = True
+        assert torch.equal(torch.isnan(out).cpu(), want)
+        clean = ~want.cuda()
+        assert torch.equal(out[clean], base[clean])
+
+
+# ---- together -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", (BF16, F32))
+def test_serving_loop(dt):
+    """A prompt appended and attended in chunks, then tokens one at a time, with
+    the window and the selected blocks joined through lse: each step equals
+    attention over the cache it stands on, and the same steps replayed from CUDA
+    graphs give the same bits."""
+    B, Hq, Hkv, d, page = 2, 8, 2, 128, 64
+    prompts, steps, T = [150, 83], 6, 256
+    p = nsa.params(B, T, Hq, Hkv, d, sel_block=page, dtype=dt, window=48, top_n=2)
+    rope = nsa.rope_table(T, d)
+    table = torch.randperm(2 * 4, generator=gen(50)).view(2, 4).to(torch.int32).cuda()
+    cache = nsa.q8_cache(p, 8, table)
+    g = gen(51)
+
+    def fresh(n):
+        return [torch.randn(n, h, d, generator=g).to(dt).cuda() for h in (Hq, Hkv, Hkv)]
+
+    done = [0, 0]
+    for chunk in (64, 100):
+        new = [min(chunk, n - x) for n, x in zip(prompts, done)]
+        q, k, v = fresh(sum(new))
+        cu = i32([0, new[0], sum(new)])
+        q_rot, _, _ = nsa.nsa_append_q8(p, k, v, i32(done), cache, cu_new=cu, q=q, rope=rope)
+        done = [x + n for x, n in zip(done, new)]
+        got = nsa.nsa_prefill_q8(p, q_rot, cache, i32(done), cu)
+        nsa.nsa_check()
+        check_attention(got, p, q_rot, cache, i32(done), cu.cpu())
+    assert done == prompts
+
+    q, k, v = fresh(B)
+    pos, lens = i32(done), i32([x + 1 for x in done])
+    sel = i32([[[0, 2], [0, 1]], [[0, 1], [1, -1]]])
+    ws = nsa.workspace(p, nsa.OP_DECODE_Q8)
+    q_rot = torch.empty_like(q)
+    bufs = {n: (torch.empty_like(q), torch.empty(B, Hq, device="cuda"))
+            for n in ("all", "window", "blocks")}
+
+    def step():
+        nsa.nsa_append_q8(p, k, v, pos, cache, q=q, q_out=q_rot, rope=rope)
+        for name, (o, s) in bufs.items():
+            nsa.nsa_decode_q8(p, q_rot, cache, lens, keys=name, out=o, lse=s, ws=ws,
+                              sel_idx=sel if name == "blocks" else None)
+
+    start = [t.clone() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+    inputs, eager = [], []
+    for i in range(steps):
+        for dst, src in zip((q, k, v), fresh(B)):
+            dst.copy_(src)
+        inputs.append([t.clone() for t in (q, k, v)])
+        step()
+        nsa.nsa_check()
+        for name, got in bufs.items():
+            check_attention(got, p, q_rot, cache, lens, None, name, sel.cpu())
+        eager.append([t.clone() for pair in bufs.values() for t in pair])
+        pos += 1
+        lens += 1
+    for dst, src in zip((cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale), start):
+        dst.copy_(src)
+    pos -= steps
+    lens -= steps
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for dst, src in zip((q, k, v), inputs[0]):
+            dst.copy_(src)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for i in range(steps):
+        for dst, src in zip((q, k, v), inputs[i]):
+            dst.copy_(src)
+        graph.replay()
+        for got, want in zip([t for pair in bufs.values() for t in pair], eager[i]):
+            assert torch.equal(got, want)
+        pos += 1
+        lens += 1
+    nsa.nsa_check()
+
+
+def test_two_streams_with_their_own_workspaces():
+    p = nsa.params(4, 3000, 16, 1, 128, sel_block=64)
+    lens = [3000, 1, 700, 2048]
+    cache = random_cache(p, lens, 60)
+    qs = [torch.randn(4, 16, 128, generator=gen(61 + i)).to(BF16).cuda() for i in range(2)]
+    want = [nsa.nsa_decode_q8(p, q, cache, i32(lens)) for q in qs]
+    L = i32(lens)
+    streams = [torch.cuda.Stream() for _ in qs]
+    wss = [nsa.workspace(p, nsa.OP_DECODE_Q8) for _ in qs]
+    outs = [[(torch.empty_like(q), torch.empty(4, 16, device="cuda")) for _ in range(20)] for q in qs]
+    torch.cuda.synchronize()
+    for r in range(20):
+        for q, s, w, o in zip(qs, streams, wss, outs):
+            nsa.nsa_decode_q8(p, q, cache, L, out=o[r][0], lse=o[r][1], ws=w, stream=s)
+    torch.cuda.synchronize()
+    for o, (out, lse) in zip(outs, want):
+        for a, b in o:
+            assert torch.equal(a, out) and torch.equal(b, lse)
+    nsa.nsa_check()
+
+
+def test_wrapper_refusals():
+    p = nsa.params(2, 100, 4, 2, 64, sel_block=32)
+    cache = random_cache(p, [100, 50], 70)
+    q = torch.zeros(2, 4, 64, dtype=BF16, device="cuda")
+    lens = i32([100, 50])
+    with pytest.raises(ValueError, match="keys"):
+        nsa.nsa_decode_q8(p, q, cache, lens, keys="some")
+    with pytest.raises(ValueError, match="q must be"):
+        nsa.nsa_decode_q8(p, q.float(), cache, lens)
+    with pytest.raises(ValueError, match="q must be"):
+        nsa.nsa_decode_q8(p, q[:1], cache, lens)
+    with pytest.raises(ValueError, match="contiguous"):
+        nsa.nsa_decode_q8(p, q.transpose(0, 1), cache, lens)
+    with pytest.raises(ValueError, match="pages are"):
+        nsa.nsa_decode_q8(nsa.params(2, 100, 4, 2, 64, sel_block=64), q, cache, lens)
+    with pytest.raises(ValueError, match="page_table"):
+        nsa.nsa_decode_q8(nsa.params(2, 200, 4, 2, 64, sel_block=32), q, cache, lens)
+    with pytest.raises(ValueError, match="sel_idx must be"):
+        nsa.nsa_decode_q8(p, q, cache, lens, keys="blocks", sel_idx=i32([[1]]))
+    with pytest.raises(nsa.NsaError, match="sel_idx"):
+        nsa.nsa_decode_q8(p, q, cache, lens, keys="blocks")
+    with pytest.raises(ValueError, match="rope_style"):
+        nsa.nsa_append_q8(p, q[:, :2].contiguous(), q[:, :2].contiguous(), lens, cache,
+                          rope=nsa.rope_table(100, 64), rope_style="other")
+    with pytest.raises(ValueError, match="pos must be"):
+        nsa.nsa_append_q8(p, q[:, :2].contiguous(), q[:, :2].contiguous(), lens[:1], cache)
