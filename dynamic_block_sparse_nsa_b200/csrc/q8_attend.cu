@@ -20,13 +20,14 @@
 // largest m_page + log2(vscale) so far (less 10, which puts p * vscale in
 // (0, 1024] and its smallest normal 2^-24 below the largest).
 //
-// Each warp streams its own contiguous share of the chunks (32 keys) through a
-// private ring of cp.async stages (no block-wide barrier in the loop); rows
-// outside the sequence, the window or the list are filled with zeros by the
-// copy, so no stale byte reaches a product. Lane (g, t) of a B fragment reads
-// 16 bytes of key g (K: 16 components, the product's k index permuted the same
-// way in q) or the same 16 components of four keys (V), so no transposition is
-// needed; the ring's chunk swizzles make both conflict-free.
+// Each warp streams its own contiguous share of the chunks (64 keys) through a
+// private ring of three cp.async slots, each K or V of a chunk, two of them in
+// flight while the third is computed on (no block-wide barrier in the loop).
+// Rows outside the sequence, the window or the list are filled with zeros by
+// the copy, so no stale byte reaches a product. Lane (g, t) of a B fragment
+// reads 16 bytes of key g (K: 16 components, the product's k index permuted
+// the same way in q) or the same 16 components of four keys (V), so no
+// transposition is needed; the slots' swizzles make both conflict-free.
 #include <algorithm>
 #include <utility>
 
@@ -39,24 +40,26 @@ using q8::Seq;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int CK = 32;       // keys per chunk
+constexpr int CK = 64;       // keys per chunk
+constexpr int NS = CK / 8;   // score tiles of 8 keys
 constexpr int ROWS = 16;     // query rows per tile
-constexpr int STAGES = 3;
+constexpr int SLOTS = 3;     // of a warp's ring
 constexpr int kSmemTiles = 1024;  // tiles whose prefix a block computes itself
 
 template <int D>
 struct Geo {
   static constexpr int TILE = CK * D;             // bytes of K or V of a chunk
-  static constexpr int RING = STAGES * 2 * TILE;  // a warp's ring
+  static constexpr int RING = SLOTS * TILE;       // a warp's ring
   static constexpr int PART = ROWS * D + ROWS;    // floats of a partial: o, lse2
   static_assert(RING >= PART * 4, "a warp's last partial goes into its ring");
 };
 
-struct StageMeta {
-  float ks[2], vs[2];
-  int kb[2];   // position of the page's first key in the chunk
+// What the computing side needs of a chunk; two chunks are under way.
+template <int PP>
+struct ChunkMeta {
+  float ks[PP], vs[PP];
+  int kb[PP];  // position of each page's first key in the chunk
   int state;   // 0: no key of the chunk is seen; 1: some; 2: every key by every row
-  int pad;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -91,7 +94,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-// Byte offset of 16-byte piece c of key r inside a K or V stage. K rows are
+// Byte offset of 16-byte piece c of key r inside a K or V slot. K rows are
 // read eight keys at a time (r, r + 4 in one quarter-warp phase), V rows four
 // (r .. r + 3) with neighbouring pieces.
 template <int D>
@@ -165,15 +168,22 @@ struct Unit {
   }
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // The copying side of a warp: its place, the pages ahead of it (one per lane)
-// and the ring.
+// and the chunk being copied.
 template <int D, int PP>
 struct Feeder {
+  static constexpr int PIECES = D / 16, RPI = 32 / PIECES;  // a copy's 512 bytes: RPI rows
   Place at;
   Unit u;
   int gbase;       // entry held by lane 0
   int pid, blk;    // this lane's page and its block number; -1: none
   float ks, vs;
+  int cp[PP], ckb[PP], coff;  // the chunk's pages, their first keys, the first key's slot
+  bool whole;                 // every row of the chunk is a live key
 
   __device__ __forceinline__ void pages(const Q8AttendArgs& a, int e, int lane) {
     gbase = e;
@@ -209,62 +219,72 @@ struct Feeder {
     gbase = INT_MIN / 2;
   }
 
-  // Copies the chunk at the place into a stage, as two groups (K, then V).
-  __device__ __forceinline__ void issue(const Q8AttendArgs& a, unsigned char* stage,
-                                        StageMeta* meta, int lane) {
+  // The pages of the chunk at the place.
+  __device__ __forceinline__ void look(const Q8AttendArgs& a, ChunkMeta<PP>* meta, int lane) {
     const int ch = at.c + (a.keys == q8::KEYS_BLOCKS ? 0 : u.lo / CK);
     const long key0 = (long)ch * CK;
     const int e = (int)(key0 / a.page);
-    const int off = PP == 1 ? (int)(key0 % a.page) : 0;
+    coff = PP == 1 ? (int)(key0 % a.page) : 0;
     if (e + PP > gbase + 32 || e < gbase) pages(a, e, lane);
-    int p[PP], kb[PP];
-    float kss[PP], vss[PP];
+    constexpr int w = CK / PP;
+    // rows of the tile see from the first token's window to the last token's
+    // position; all of them see [full_lo, full_hi)
+    const int t0 = u.r0 / a.G, t1 = min(u.s.n - 1, (u.r0 + ROWS - 1) / a.G);
+    const int at0 = u.s.len - u.s.n;
+    const int full_hi = u.hi > 0 ? at0 + t0 + 1 : 0;
+    const int full_lo = a.keys == q8::KEYS_WINDOW ? at0 + t1 + 1 - a.window : 0;
+    bool some = false, full = true;
+    whole = true;
 #pragma unroll
     for (int i = 0; i < PP; ++i) {
       const int src = e - gbase + i;
-      p[i] = __shfl_sync(0xffffffffu, pid, src);
-      kb[i] = __shfl_sync(0xffffffffu, blk, src) * a.page + off;
-      kss[i] = __shfl_sync(0xffffffffu, ks, src);
-      vss[i] = __shfl_sync(0xffffffffu, vs, src);
-      if (p[i] < 0) kb[i] = INT_MAX / 2;  // past every row
-    }
-    if (lane == 0) {
-      // rows of the tile see from the first token's window to the last token's
-      // position; all of them see [full_lo, full_hi)
-      const int t0 = u.r0 / a.G, t1 = min(u.s.n - 1, (u.r0 + ROWS - 1) / a.G);
-      const int at0 = u.s.len - u.s.n;
-      const int full_hi = u.hi > 0 ? at0 + t0 + 1 : 0;
-      const int full_lo = a.keys == q8::KEYS_WINDOW ? at0 + t1 + 1 - a.window : 0;
-      bool some = false, full = true;
-#pragma unroll
-      for (int i = 0; i < PP; ++i) {
-        const int w = CK / PP;
-        some |= kb[i] < u.hi && kb[i] + w > u.lo;
-        full &= kb[i] >= full_lo && kb[i] + w <= full_hi;
-        meta->ks[i] = kss[i];
-        meta->vs[i] = vss[i];
-        meta->kb[i] = kb[i];
+      cp[i] = __shfl_sync(0xffffffffu, pid, src);
+      ckb[i] = __shfl_sync(0xffffffffu, blk, src) * a.page + coff;
+      const float k = __shfl_sync(0xffffffffu, ks, src), v = __shfl_sync(0xffffffffu, vs, src);
+      if (cp[i] < 0) ckb[i] = INT_MAX / 2;  // past every row
+      some |= ckb[i] < u.hi && ckb[i] + w > u.lo;
+      full &= ckb[i] >= full_lo && ckb[i] + w <= full_hi;
+      whole &= ckb[i] >= u.lo && ckb[i] + w <= u.hi;
+      if (lane == 0) {
+        meta->ks[i] = k;
+        meta->vs[i] = v;
+        meta->kb[i] = ckb[i];
       }
-      meta->state = some ? (full ? 2 : 1) : 0;
     }
-    constexpr int PIECES = D / 16, RPI = 32 / PIECES;
+    if (lane == 0) meta->state = some ? (full ? 2 : 1) : 0;
+  }
+
+  // Copies K or V of the chunk into a slot.
+  template <bool V>
+  __device__ __forceinline__ void copy(const Q8AttendArgs& a, uint32_t slot, int lane) {
     const int c = lane % PIECES, rl = lane / PIECES;
+    const uint8_t* base = V ? a.v_pages : a.k_pages;
+    // copy i's rows lie 512 i bytes behind copy 0's, in the page and in the
+    // slot, but for the bit of a K row's swizzle that alternates
+    const uint32_t d0 = slot + (V ? v_off<D>(rl, c) : k_off<D>(rl, c));
+    const uint32_t d1 = D == 128 && !V ? d0 ^ 64 : d0;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* base = kv ? a.v_pages : a.k_pages;
-      unsigned char* dst = stage + kv * Geo<D>::TILE;
+    for (int p = 0; p < PP; ++p) {
+      const uint8_t* src =
+          base + (((long)cp[p] * a.Hkv + at.h) * a.page + coff + rl) * D + c * 16;
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < CK / RPI; ++i) {
-        const int r = i * RPI + rl;
-        const int pi = PP == 1 ? 0 : i * RPI / (CK / PP);  // (a copy's rows lie in one page)
-        const int slot = PP == 1 ? off + r : r % (CK / PP);
-        const int pos = kb[pi] + (PP == 1 ? r : slot);
-        const bool live = pos >= u.lo && pos < u.hi;
-        const uint8_t* src = base;
-        if (live) src += (((long)p[pi] * a.Hkv + at.h) * a.page + slot) * D + c * 16;
-        ptx::cp_async16_zfill(dst + (kv ? v_off<D>(r, c) : k_off<D>(r, c)), src, live ? 16 : 0);
+        for (int k = 0; k < CK / PP / RPI; ++k) {
+          const int i = p * (CK / PP / RPI) + k;
+          cp_async16((i & 1 ? d1 : d0) + 512 * i, src + 512 * k);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < CK / PP / RPI; ++k) {
+          const int i = p * (CK / PP / RPI) + k;
+          const int pos = ckb[p] + k * RPI + rl;
+          const bool live = pos >= u.lo && pos < u.hi;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((i & 1 ? d1 : d0) +
+                                                                               512 * i),
+                       "l"(live ? src + 512 * k : base), "r"(live ? 16 : 0)
+                       : "memory");
+        }
       }
-      ptx::cp_async_commit();
     }
   }
 
@@ -283,7 +303,7 @@ struct Rows {
   static constexpr int KS = D / 16;  // product steps of 16 components
   static constexpr int NT = D / 8;   // output tiles of 8 components
   uint32_t q[PARTS][KS][4];
-  float qf[2];        // row factor of the scores: 2^shift * softmax_scale * log2(e)
+  float qf[2];        // row factor of the scores (> 0): 2^shift * |softmax_scale| * log2(e)
   int lo[2], hi[2];   // keys the lane's two rows see
   float o[NT][4];
   float m[2], l[2], M[2];
@@ -329,8 +349,9 @@ struct Rows {
       // 2^up brings the largest component to [2^14, 2^15)
       int up = big > 0.f ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
       up = min(max(up, -120), 120);
-      const float mul = q8::exp2_int(up);
-      qf[i] = q8::exp2_int(-up) * a.scale_log2;
+      // (a negative softmax scale's sign goes into q)
+      const float mul = a.scale_log2 < 0.f ? -q8::exp2_int(up) : q8::exp2_int(up);
+      qf[i] = q8::exp2_int(-up) * fabsf(a.scale_log2);
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -348,62 +369,62 @@ struct Rows {
     }
   }
 
-  // z[nt][.]: scores of keys 8 nt + t, 8 nt + t + 4 for rows g (0, 1) and g + 8 (2, 3)
-  __device__ __forceinline__ void scores(float (&z)[4][4], uint32_t kbase, int lane) {
+  // z[nt][.]: q . kcode of keys 8 nt + t, 8 nt + t + 4 for rows g (0, 1) and g + 8 (2, 3)
+  __device__ __forceinline__ void scores(float (&z)[NS][4], uint32_t kbase, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const int kr = (g >> 1) | ((g & 1) << 2);
+    const uint32_t k0 = kbase + k_off<D>((g >> 1) | ((g & 1) << 2), t);
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
+    for (int nt = 0; nt < NS; ++nt) {
       z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.f;
+      float low[4] = {0.f, 0.f, 0.f, 0.f};  // of q's second part: summed apart
 #pragma unroll
       for (int half = 0; half < D / 64; ++half) {
-        const uint4 v = lds128(kbase + k_off<D>(8 * nt + kr, 4 * half + t));
+        const uint4 v = lds128((half ? k0 ^ 64 : k0) + nt * 8 * D);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t b0 = q8::e4m3x2_to_half2((uint16_t)(w[j] & 0xffffu));
           const uint32_t b1 = q8::e4m3x2_to_half2((uint16_t)(w[j] >> 16));
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) mma_f16(z[nt], q[p][4 * half + j], b0, b1);
+          mma_f16(z[nt], q[0][4 * half + j], b0, b1);
+          if (PARTS == 2) mma_f16(low, q[PARTS - 1][4 * half + j], b0, b1);
         }
+      }
+      if (PARTS == 2) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[nt][x] += low[x];
       }
     }
   }
 
   // Running softmax: z becomes p * vscale in units of 2^M; o, l, m, M follow.
   template <int PP>
-  __device__ __forceinline__ void softmax(float (&z)[4][4], const StageMeta& meta, bool full,
+  __device__ __forceinline__ void softmax(float (&z)[NS][4], const ChunkMeta<PP>& meta, bool full,
                                           int lane) {
     const int t = lane & 3;
-    constexpr int TP = 4 / PP;  // score tiles of a page
-    float lv[PP];               // log2 of the value scales
-#pragma unroll
-    for (int p = 0; p < PP; ++p) lv[p] = __log2f(meta.vs[p]);
+    constexpr int TP = NS / PP;  // score tiles of a page
     if (!full) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int nt = 0; nt < NS; ++nt)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int i = x >> 1;
           const int key = meta.kb[nt / TP] + 8 * (nt % TP) + t + 4 * (x & 1);
-          z[nt][x] = key >= lo[i] && key < hi[i] ? z[nt][x] * (qf[i] * meta.ks[nt / TP]) : -INFINITY;
+          if (key < lo[x >> 1] || key >= hi[x >> 1]) z[nt][x] = -INFINITY;
         }
-    } else {
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) z[nt][x] *= qf[x >> 1] * meta.ks[nt / TP];
     }
+    float lv[PP];  // log2 of the value scales
+#pragma unroll
+    for (int p = 0; p < PP; ++p) lv[p] = __log2f(meta.vs[p]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float top = m[i], ref = M[i];
+      float top = m[i], ref = M[i], c[PP];
 #pragma unroll
       for (int p = 0; p < PP; ++p) {
+        c[p] = fmaxf(qf[i] * meta.ks[p], 1.17549435e-38f);  // (a masked -inf stays -inf)
         float pm = -INFINITY;
 #pragma unroll
         for (int nt = p * TP; nt < (p + 1) * TP; ++nt)
           pm = fmaxf(pm, fmaxf(z[nt][2 * i], z[nt][2 * i + 1]));
-        pm = quad_max(pm);
+        pm = quad_max(pm) * c[p];
         top = fmaxf(top, pm);
         ref = fmaxf(ref, pm + fmaxf(lv[p], -126.f) - 10.f);
       }
@@ -412,32 +433,38 @@ struct Rows {
       const float al = ptx::ex2(m[i] - base), ao = ptx::ex2(M[i] - oref);
       m[i] = top;
       M[i] = ref;
+      // p * vscale * 2^-M = 2^(z2 + log2(vscale) - M); p itself, for l, is
+      // that times 2^-e, e = m + log2(vscale) - M
       float sum = 0.f;
-      bool far = false;
+      bool apart = fabsf(base) > 4194304.f;
 #pragma unroll
-      for (int p = 0; p < PP; ++p) far |= base - oref + lv[p] > 100.f;
-      if (__any_sync(0xffffffffu, far)) {
-        // a page of much larger values than the others' that is hardly
-        // attended: p would leave fp32's range before its scale brings it back
+      for (int p = 0; p < PP; ++p) apart |= !(base - oref + lv[p] > -60.f);
+      if (__any_sync(0xffffffffu, apart)) {
+        // p for itself, from a rounded score: a page of far smaller values than
+        // the others', whose p * vscale vanishes and p does not; or scores so
+        // large that the exact z2 - m of a fused product is not 0 at the maximum
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < NS; ++nt)
 #pragma unroll
           for (int x = 2 * i; x < 2 * i + 2; ++x) {
-            sum += ptx::ex2(z[nt][x] - base);
-            z[nt][x] = ptx::ex2(z[nt][x] - oref + lv[nt / TP]);
+            const float d = __fadd_rn(__fmul_rn(z[nt][x], c[nt / TP]), -base);
+            sum += ptx::ex2(d);
+            z[nt][x] = ptx::ex2(d + (base - oref + lv[nt / TP]));
           }
       } else {
-        float f[PP];
 #pragma unroll
-        for (int p = 0; p < PP; ++p) f[p] = ptx::ex2(base - oref + lv[p]);
+        for (int p = 0; p < PP; ++p) {
+          const float off = lv[p] - oref;
+          float ps = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+          for (int nt = p * TP; nt < (p + 1) * TP; ++nt)
 #pragma unroll
-          for (int x = 2 * i; x < 2 * i + 2; ++x) {
-            const float p = ptx::ex2(z[nt][x] - base);
-            sum += p;
-            z[nt][x] = p * f[nt / TP];
-          }
+            for (int x = 2 * i; x < 2 * i + 2; ++x) {
+              z[nt][x] = ptx::ex2(fmaf(z[nt][x], c[p], off));
+              ps += z[nt][x];
+            }
+          sum = fmaf(ps, ptx::ex2(oref - base - lv[p]), sum);
+        }
       }
       l[i] = l[i] * al + sum;
       if (__any_sync(0xffffffffu, ao != 1.f)) {
@@ -450,63 +477,103 @@ struct Rows {
     }
   }
 
-  __device__ __forceinline__ void values(const float (&z)[4][4], uint32_t vbase, int lane) {
+  // Fragment x of P's k step s: rows g, g + 8 of keys t, t + 4 (x = 0, 1), of 8 + t, 12 + t
+  static __device__ __forceinline__ void weights(uint32_t (&a)[PARTS][4], const float (&z)[NS][4],
+                                                 int s) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float p0 = z[2 * s + (x >> 1)][2 * (x & 1)], p1 = z[2 * s + (x >> 1)][2 * (x & 1) + 1];
+      a[0][x] = pack_half(p0, p1);
+      if (PARTS == 2) {
+        const float2 f = unpack_half(a[0][x]);
+        a[PARTS - 1][x] = pack_half(p0 - f.x, p1 - f.y);
+      }
+    }
+  }
+
+  // Word k of the lane's pieces of keys t, 4 + t, 8 + t, 12 + t (its components
+  // 4 k .. 4 k + 3) as the B fragments of output tiles 4 k .. 4 k + 3.
+  static __device__ __forceinline__ void fragments(const uint32_t (&w)[4], uint32_t (&b)[4][2]) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const uint32_t sel = y ? 0x7362u : 0x5140u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = __byte_perm(w[2 * h], w[2 * h + 1], sel);
+        b[2 * y][h] = q8::e4m3x2_to_half2((uint16_t)(x & 0xffffu));
+        b[2 * y + 1][h] = q8::e4m3x2_to_half2((uint16_t)(x >> 16));
+      }
+    }
+  }
+
+  __device__ __forceinline__ void values(const float (&z)[NS][4], uint32_t vbase, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    const uint32_t v0 = vbase + (D == 128 ? v_off<D>(t, g) : v_off<D>(t, g >> 1) + (g & 1) * 8);
+    if (PARTS == 1) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t a[PARTS][4];
+      for (int s = 0; s < CK / 16; ++s) {
+        uint32_t a[PARTS][4];
+        weights(a, z, s);
+        uint32_t w[4][D / 32];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        // a0, a1: rows g, g + 8 of keys t, t + 4; a2, a3: of keys 8 + t, 12 + t
-        const float p0 = z[2 * s + (x >> 1)][2 * (x & 1)], p1 = z[2 * s + (x >> 1)][2 * (x & 1) + 1];
-        a[0][x] = pack_half(p0, p1);
-        if (PARTS == 2) {
-          const float2 f = unpack_half(a[0][x]);
-          a[PARTS - 1][x] = pack_half(p0 - f.x, p1 - f.y);
-        }
-      }
-      uint32_t w[4][D / 32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * s + 4 * i + t;
-        if (D == 128) {
-          const uint4 v = lds128(vbase + v_off<D>(r, g));
-          w[i][0] = v.x;
-          w[i][1] = v.y;
-          w[i][D / 32 - 2] = v.z;
-          w[i][D / 32 - 1] = v.w;
-        } else {
-          const uint2 v = lds64(vbase + v_off<D>(r, g >> 1) + (g & 1) * 8);
-          w[i][0] = v.x;
-          w[i][1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t sel = y ? 0x7362u : 0x5140u;
-          const uint32_t x0 = __byte_perm(w[0][k], w[1][k], sel);
-          const uint32_t x1 = __byte_perm(w[2][k], w[3][k], sel);
-          const uint32_t b00 = q8::e4m3x2_to_half2((uint16_t)(x0 & 0xffffu));
-          const uint32_t b01 = q8::e4m3x2_to_half2((uint16_t)(x1 & 0xffffu));
-          const uint32_t b10 = q8::e4m3x2_to_half2((uint16_t)(x0 >> 16));
-          const uint32_t b11 = q8::e4m3x2_to_half2((uint16_t)(x1 >> 16));
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            mma_f16(o[4 * k + 2 * y], a[p], b00, b01);
-            mma_f16(o[4 * k + 2 * y + 1], a[p], b10, b11);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = v0 + (16 * s + 4 * i) * D;
+          if (D == 128) {
+            const uint4 v = lds128(at);
+            w[i][0] = v.x;
+            w[i][1] = v.y;
+            w[i][D / 32 - 2] = v.z;
+            w[i][D / 32 - 1] = v.w;
+          } else {
+            const uint2 v = lds64(at);
+            w[i][0] = v.x;
+            w[i][1] = v.y;
           }
         }
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const uint32_t wk[4] = {w[0][k], w[1][k], w[2][k], w[3][k]};
+          uint32_t b[4][2];
+          fragments(wk, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_f16(o[4 * k + j], a[0], b[j][0], b[j][1]);
+        }
+      }
+    } else {
+      // fp32: the tensor core's sums of a chunk are short, and added to o in
+      // fp32 with rounding to nearest (its own additions truncate)
+      uint32_t a[CK / 16][PARTS][4];
+#pragma unroll
+      for (int s = 0; s < CK / 16; ++s) weights(a[s], z, s);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        float add[4][4] = {};
+#pragma unroll
+        for (int s = 0; s < CK / 16; ++s) {
+          uint32_t wk[4], b[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(wk[i]) : "r"(v0 + (16 * s + 4 * i) * D + 4 * k));
+          fragments(wk, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int p = PARTS - 1; p >= 0; --p) mma_f16(add[j], a[s][p], b[j][0], b[j][1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[4 * k + j][x] += add[j][x];
+      }
     }
   }
 
   // Values that are NaN in keys which some rows of the tile see and others do
   // not: 0 * NaN must not reach the rows that do not. Their codes become zeros
-  // in the stage and the rows that see them become NaN. Rare, and only in
+  // in the slot and the rows that see them become NaN. Rare, and only in
   // chunks on the edge of a row's keys.
   template <int PP>
-  __device__ void nan_values(unsigned char* vst, const StageMeta& meta, int lane) {
+  __device__ void nan_values(unsigned char* vst, const ChunkMeta<PP>& meta, int lane) {
     bool found = false;
     for (int i = lane; i < CK * D / 16; i += 32) {
       const uint4 v = reinterpret_cast<const uint4*>(vst)[i];
@@ -517,6 +584,7 @@ struct Rows {
     if (!__any_sync(0xffffffffu, found)) return;
     const int t = lane & 3;
     constexpr int RUN = D / 4;  // the lane's outputs are components RUN t .. of its rows
+#pragma unroll 1
     for (int r = 0; r < CK; ++r) {
       const int key = meta.kb[r / (CK / PP)] + r % (CK / PP);
 #pragma unroll
@@ -609,19 +677,21 @@ struct Segment {
   const float* part;
 };
 
-template <typename T, int D>
+template <typename T, int D, int PP>
 struct Smem {
   static constexpr int RING = kWarps * Geo<D>::RING;
   static constexpr int META = RING;
-  static constexpr int SEGS = META + kWarps * STAGES * (int)sizeof(StageMeta);
+  static constexpr int SEGS = (META + kWarps * 2 * (int)sizeof(ChunkMeta<PP>) + 15) / 16 * 16;
   static constexpr int SUMS = SEGS + 2 * kWarps * (int)sizeof(Segment);
   static constexpr int PRE = SUMS + kWarps * 8;
   static constexpr int BYTES = PRE + (kSmemTiles + 1) * 8;
 };
 
-template <typename T, int D, int PP>
-__global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const Q8AttendArgs a) {
-  using S = Smem<T, D>;
+// MULTI: a tile can hold several tokens, which see different keys.
+template <typename T, int D, int PP, bool MULTI>
+__global__ void __launch_bounds__(kThreads, 1)
+    q8_attend_kernel(const __grid_constant__ Q8AttendArgs a) {
+  using S = Smem<T, D, PP>;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
@@ -689,62 +759,63 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const Q8AttendAr
   const long x0 = X0 + (X1 - X0) * warp / kWarps, x1 = X0 + (X1 - X0) * (warp + 1) / kWarps;
 
   if (x1 > x0) {
+    constexpr int TILE = Geo<D>::TILE;
     unsigned char* ring = smem + warp * Geo<D>::RING;
-    StageMeta* meta = reinterpret_cast<StageMeta*>(smem + S::META) + warp * STAGES;
+    ChunkMeta<PP>* meta = reinterpret_cast<ChunkMeta<PP>*>(smem + S::META) + warp * 2;
     const uint32_t ring_u = ptx::smem_u32(ring);
     Feeder<D, PP> feed;
     feed.start(a, pl, x0);
-    long fx = x0;
     Place at = feed.at;
     Unit u = feed.u;
-#pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k) {
-      if (fx < x1) {
-        feed.issue(a, ring + k * 2 * Geo<D>::TILE, meta + k, lane);
-        if (++fx < x1) feed.next(a, pl);
-      } else {
-        ptx::cp_async_commit();
-        ptx::cp_async_commit();
-      }
-    }
+    // K and V of the first chunk into slots 0 and 1
+    feed.look(a, meta, lane);
+    feed.template copy<false>(a, ring_u, lane);
+    ptx::cp_async_commit();
+    feed.template copy<true>(a, ring_u + TILE, lane);
+    ptx::cp_async_commit();
     Rows<T, D> rows;
     rows.load(a, u, at.h, lane);
     rows.clear();
     bool whole = at.c == 0;  // the unit's first chunk is the warp's
-    int st = 0;
-    for (long x = x0; x < x1; ++x) {
-      ptx::cp_async_wait<2 * (STAGES - 2) + 1>();
+    int sk = 0;              // slot of the chunk's K; its V is in the next, the next K behind that
+    int mi = 0;
+    const int len = (int)(x1 - x0);
+    for (int x = 0; x < len; ++x) {
+      const int sv = sk + 1 == SLOTS ? 0 : sk + 1, sn = sv + 1 == SLOTS ? 0 : sv + 1;
+      ptx::cp_async_wait<1>();  // K
       __syncwarp();
-      const int nx = st == 0 ? STAGES - 1 : st - 1;
-      if (fx < x1) {
-        feed.issue(a, ring + nx * 2 * Geo<D>::TILE, meta + nx, lane);
-        if (++fx < x1) feed.next(a, pl);
-      } else {
-        ptx::cp_async_commit();
-        ptx::cp_async_commit();
+      const bool more = x + 1 < len;
+      if (more) {
+        feed.next(a, pl);
+        feed.look(a, meta + (mi ^ 1), lane);
+        feed.template copy<false>(a, ring_u + sn * TILE, lane);
       }
-      const StageMeta sm = meta[st];
-      float z[4][4];
-      if (sm.state) {
-        rows.scores(z, ring_u + st * 2 * Geo<D>::TILE, lane);
-        rows.template softmax<PP>(z, sm, sm.state == 2, lane);
+      ptx::cp_async_commit();
+      const ChunkMeta<PP>& sm = meta[mi];
+      const int state = sm.state;
+      float z[NS][4];
+      if (state) {
+        rows.scores(z, ring_u + sk * TILE, lane);
+        rows.template softmax<PP>(z, sm, state == 2, lane);
       }
-      ptx::cp_async_wait<2 * (STAGES - 1)>();
+      ptx::cp_async_wait<1>();  // V
       __syncwarp();
-      if (sm.state) {
-        const uint32_t vb = ring_u + st * 2 * Geo<D>::TILE + Geo<D>::TILE;
-        if (sm.state == 1 && a.cu)
-          rows.template nan_values<PP>(ring + st * 2 * Geo<D>::TILE + Geo<D>::TILE, sm, lane);
-        rows.values(z, vb, lane);
+      if (more) feed.template copy<true>(a, ring_u + sk * TILE, lane);
+      ptx::cp_async_commit();
+      if (state) {
+        if (MULTI && state == 1)
+          rows.template nan_values<PP>(ring + sv * TILE, sm, lane);
+        rows.values(z, ring_u + sv * TILE, lane);
       }
-      st = st + 1 == STAGES ? 0 : st + 1;
+      sk = sn;
+      mi ^= 1;
       const bool last = at.c + 1 == at.nc;
-      if (last || x + 1 == x1) {
+      if (last || !more) {
         float lse2[2];
         rows.finish(lse2);
         if (whole && last) {
           rows.write(a, u, at.h, lse2, lane);
-        } else if (x + 1 < x1) {
+        } else if (more) {
           float* part = a.hold + ((long)cta * kWarps + warp) * Geo<D>::PART;
           rows.store(part, lse2, lane);
           if (lane == 0) segs[2 * warp] = Segment{at.tile, at.h, part};
@@ -755,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const Q8AttendAr
           rows.store(part, lse2, lane);
           if (lane == 0) segs[2 * warp + 1] = Segment{at.tile, at.h, part};
         }
-        if (x + 1 < x1) {
+        if (more) {
           const int tile = at.tile;
           at.next(pl, a.Hkv);
           if (at.tile != tile) u.load(a, pl, at.tile);
@@ -797,9 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const Q8AttendAr
     }
     Unit u;
     if (done) u.load(a, pl, tile);
-#pragma unroll
-    for (int rr = 0; rr < ROWS / kWarps; ++rr) {
-      const int r = warp * (ROWS / kWarps) + rr;
+#pragma unroll 2
+    for (int r = warp; r < ROWS; r += kWarps) {
       float top = -INFINITY;
       for (int e = k; e < end; ++e)
         if (segs[e].tile >= 0) top = fmaxf(top, segs[e].part[ROWS * D + r]);
@@ -979,8 +1049,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 
 template <typename T, int D, int PP>
 cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
-  auto kern = q8_attend_kernel<T, D, PP>;
-  constexpr int smem = Smem<T, D>::BYTES;
+  auto kern = a.cu ? q8_attend_kernel<T, D, PP, true> : q8_attend_kernel<T, D, PP, false>;
+  constexpr int smem = Smem<T, D, PP>::BYTES;
   cudaError_t e;
   if ((e = ensure_dyn_smem((const void*)kern, smem)) != cudaSuccess) return e;
   {
@@ -990,6 +1060,12 @@ cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
   }
   TraceScope trace("q8_merge", stream);
   return launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, ROWS), dim3(128), 0, stream, a, ROWS);
+}
+
+template <typename T, int D>
+cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
+  if (a.page >= CK) return launch<T, D, 1>(a, stream);
+  return a.page == 32 ? launch<T, D, 2>(a, stream) : launch<T, D, 4>(a, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1059,13 +1135,8 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
   }
   const bool bf16 = p.dtype == NSA_DTYPE_BF16;
   using bf = __nv_bfloat16;
-  if (p.d == 128) {
-    if (a.page >= CK)
-      return bf16 ? launch<bf, 128, 1>(a, stream) : launch<float, 128, 1>(a, stream);
-    return bf16 ? launch<bf, 128, 2>(a, stream) : launch<float, 128, 2>(a, stream);
-  }
-  if (a.page >= CK) return bf16 ? launch<bf, 64, 1>(a, stream) : launch<float, 64, 1>(a, stream);
-  return bf16 ? launch<bf, 64, 2>(a, stream) : launch<float, 64, 2>(a, stream);
+  if (p.d == 128) return bf16 ? launch<bf, 128>(a, stream) : launch<float, 128>(a, stream);
+  return bf16 ? launch<bf, 64>(a, stream) : launch<float, 64>(a, stream);
 }
 
 }  // namespace nsa

@@ -439,16 +439,22 @@ class Q8Cache:
         self.k_pages, self.v_pages = k_pages, v_pages
         self.k_scale, self.v_scale, self.page_table = k_scale, v_scale, page_table
         self.device = dev
+        self._p = None  # the parameters last found to fit
         self.c = NsaQ8Cache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
                             v_scale.data_ptr(), page_table.data_ptr(), k_pages.shape[0])
+        self.ref = ctypes.byref(self.c)
 
     def _fits(self, p):
+        need = (p.B, p.T, p.Hkv, p.sel_block, p.d)
+        if need == self._p:
+            return
         if self.k_pages.shape[1:] != (p.Hkv, p.sel_block, p.d):
             raise ValueError(f"pages are {tuple(self.k_pages.shape[1:])}, the parameters say "
                              f"{(p.Hkv, p.sel_block, p.d)} (Hkv, sel_block, d)")
         if self.page_table.shape != (p.B, -(-p.T // p.sel_block)):
             raise ValueError(f"page_table is {tuple(self.page_table.shape)}, the parameters need "
                              f"{(p.B, -(-p.T // p.sel_block))}")
+        self._p = need
 
 
 def q8_cache(p, num_pages, page_table):
@@ -478,44 +484,70 @@ def _shape(t, name, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _is(t, name, dtype, device, shape):
+    """_dev and _shape in one, as cheap as a decode step wants its checks."""
+    if t is None or (t.dtype is dtype and t.device == device and t.shape == shape
+                     and t.is_contiguous()):
+        return
+    _dev(t, name, dtype, device)
+    _shape(t, name, shape)
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current (as _on and _stream)."""
+    index = device.index
+    if stream is None and torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with _on(device):
+            st = fn(*args, _stream(stream, device))
+    if st != NSA_OK:
+        _raise(st)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def nsa_append_q8(p, k_new, v_new, pos, cache, cu_new=None, q=None, rope=None, rope_style="half",
                   q_out=None, k_out=None, v_out=None, want_kv=False, stream=None):
     """Append tokens k_new, v_new [N, Hkv, d] at positions pos[b] + i of the 8-bit
     cache, keys (and q [N, Hq, d]) rotated by rope [len, 2, dim / 2] (see
     rope_table). Returns (q_out, k_out, v_out): the rotated queries, and the
     tokens as the cache holds them with want_kv (else None, unless given)."""
-    dt = p.torch_dtype
-    _dev(k_new, "k_new", dt, cache.device)
-    dev = cache.device
+    dt, dev = p.torch_dtype, cache.device
     cache._fits(p)
     N = k_new.shape[0]
     kv, qs = (N, p.Hkv, p.d), (N, p.Hq, p.d)
+    _is(k_new, "k_new", dt, dev, kv)
+    _is(v_new, "v_new", dt, dev, kv)
+    _is(q, "q", dt, dev, qs)
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
-    if want_kv:
-        k_out = torch.empty_like(k_new) if k_out is None else k_out
-        v_out = torch.empty_like(k_new) if v_out is None else v_out
-    for t, nm, shape in ((k_new, "k_new", kv), (v_new, "v_new", kv), (q, "q", qs),
-                         (q_out, "q_out", qs), (k_out, "k_out", kv), (v_out, "v_out", kv)):
-        _dev(t, nm, dt, dev)
-        _shape(t, nm, shape)
-    _dev(pos, "pos", torch.int32, dev)
-    _shape(pos, "pos", (p.B,))
-    _dev(cu_new, "cu_new", torch.int32, dev)
-    _shape(cu_new, "cu_new", (p.B + 1,))
+    else:
+        _is(q_out, "q_out", dt, dev, qs)
+    if want_kv and k_out is None:
+        k_out = torch.empty_like(k_new)
+    else:
+        _is(k_out, "k_out", dt, dev, kv)
+    if want_kv and v_out is None:
+        v_out = torch.empty_like(k_new)
+    else:
+        _is(v_out, "v_out", dt, dev, kv)
+    _is(pos, "pos", torch.int32, dev, (p.B,))
+    _is(cu_new, "cu_new", torch.int32, dev, (p.B + 1,))
     turn = None
     if rope is not None:
-        _dev(rope, "rope", torch.float32, dev)
+        if rope.dtype is not torch.float32 or rope.device != dev or not rope.is_contiguous():
+            _dev(rope, "rope", torch.float32, dev)
         if rope.dim() != 3 or rope.shape[1] != 2:
             raise ValueError(f"rope must be [len, 2, dim / 2], got {list(rope.shape)}")
         if rope_style not in ROPE_STYLES:
             raise ValueError(f"rope_style must be one of {sorted(ROPE_STYLES)}")
         turn = ctypes.byref(NsaRope(rope.data_ptr(), rope.shape[0], 2 * rope.shape[2],
                                     ROPE_STYLES[rope_style]))
-    with _on(dev):
-        _raise(LIB.nsa_append_q8(ctypes.byref(p), ctypes.byref(cache.c), _ptr(k_new), _ptr(v_new),
-                                 N, _ptr(pos), _ptr(cu_new), turn, _ptr(q), _ptr(q_out),
-                                 _ptr(k_out), _ptr(v_out), _stream(stream, dev)))
+    _call(LIB.nsa_append_q8, dev, stream, ctypes.byref(p), cache.ref, _addr(k_new), _addr(v_new), N,
+          _addr(pos), _addr(cu_new), turn, _addr(q), _addr(q_out), _addr(k_out), _addr(v_out))
     return q_out, k_out, v_out
 
 
@@ -526,20 +558,20 @@ def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op):
     if keys not in KEYS:
         raise ValueError(f"keys must be one of {sorted(KEYS)}")
     shape = (N, p.Hq, p.d)
+    _is(q, "q", dt, dev, shape)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = torch.empty_like(q)
+    else:
+        _is(out, "out", dt, dev, shape)
     if lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-    for t, nm in ((q, "q"), (out, "out")):
-        _dev(t, nm, dt, dev)
-        _shape(t, nm, shape)
-    _dev(lse, "lse", torch.float32, dev)
-    _shape(lse, "lse", shape[:2])
-    _dev(seq_lens, "seq_lens", torch.int32, dev)
-    _shape(seq_lens, "seq_lens", (p.B,))
+    else:
+        _is(lse, "lse", torch.float32, dev, shape[:2])
+    _is(seq_lens, "seq_lens", torch.int32, dev, (p.B,))
     if ws is None:
         ws = workspace(p, op, dev)
-    _dev(ws, "ws", None, dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _dev(ws, "ws", None, dev)
     return out, lse, ws, ws.numel() * ws.element_size()
 
 
@@ -551,12 +583,9 @@ def nsa_decode_q8(p, q, cache, seq_lens, keys="all", sel_idx=None, out=None, lse
     out, lse, ws, nbytes = _attend_q8_args(p, q, p.B, cache, seq_lens, keys, out, lse, ws,
                                            OP_DECODE_Q8)
     dev = cache.device
-    _dev(sel_idx, "sel_idx", torch.int32, dev)
-    _shape(sel_idx, "sel_idx", (p.B, p.Hkv, p.top_n))
-    with _on(dev):
-        _raise(LIB.nsa_decode_q8(ctypes.byref(p), ctypes.byref(cache.c), _ptr(q), _ptr(seq_lens),
-                                 KEYS[keys], _ptr(sel_idx), _ptr(out), _ptr(lse), _ptr(ws), nbytes,
-                                 _stream(stream, dev)))
+    _is(sel_idx, "sel_idx", torch.int32, dev, (p.B, p.Hkv, p.top_n))
+    _call(LIB.nsa_decode_q8, dev, stream, ctypes.byref(p), cache.ref, _addr(q), _addr(seq_lens),
+          KEYS[keys], _addr(sel_idx), _addr(out), _addr(lse), _addr(ws), nbytes)
     return out, lse
 
 
@@ -569,12 +598,9 @@ def nsa_prefill_q8(p, q, cache, seq_lens, cu_q=None, keys="all", out=None, lse=N
     out, lse, ws, nbytes = _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws,
                                            OP_PREFILL_Q8)
     dev = cache.device
-    _dev(cu_q, "cu_q", torch.int32, dev)
-    _shape(cu_q, "cu_q", (p.B + 1,))
-    with _on(dev):
-        _raise(LIB.nsa_prefill_q8(ctypes.byref(p), ctypes.byref(cache.c), _ptr(q), N, _ptr(cu_q),
-                                  _ptr(seq_lens), KEYS[keys], _ptr(out), _ptr(lse), _ptr(ws),
-                                  nbytes, _stream(stream, dev)))
+    _is(cu_q, "cu_q", torch.int32, dev, (p.B + 1,))
+    _call(LIB.nsa_prefill_q8, dev, stream, ctypes.byref(p), cache.ref, _addr(q), N, _addr(cu_q),
+          _addr(seq_lens), KEYS[keys], _addr(out), _addr(lse), _addr(ws), nbytes)
     return out, lse
 
 
