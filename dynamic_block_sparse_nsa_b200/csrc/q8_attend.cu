@@ -122,6 +122,7 @@ struct Plan {
   const long* pre;   // chunks (times KV heads) before each tile, [tiles + 1]
   const int* tseq;   // sequence of each tile; null: tile / rt
   const int* tbase;  // first tile of each sequence (with tseq)
+  const int* lens;   // without tseq: length of each tile's sequence; -1: a bad one
   int tiles, rt;
 };
 
@@ -161,9 +162,19 @@ struct Unit {
   int b, r0, lo, hi;
   Seq s;
   __device__ __forceinline__ void load(const Q8AttendArgs& a, const Plan& pl, int tile) {
-    b = pl.tseq ? pl.tseq[tile] : tile / pl.rt;
-    r0 = (tile - (pl.tseq ? pl.tbase[b] : b * pl.rt)) * ROWS;
-    s = q8::sequence(a, b);
+    if (pl.tseq) {
+      b = pl.tseq[tile];
+      r0 = (tile - pl.tbase[b]) * ROWS;
+      s = q8::sequence(a, b);
+    } else {
+      b = tile / pl.rt;
+      r0 = (tile - b * pl.rt) * ROWS;
+      s.first = b;
+      s.n = 1;
+      s.len = pl.lens[tile];
+      s.ok = s.len >= 0;
+      if (!s.ok) s.len = 0;
+    }
     q8::key_span(a, s, r0, ROWS, lo, hi);
   }
 };
@@ -183,6 +194,7 @@ struct Feeder {
   int pid, blk;    // this lane's page and its block number; -1: none
   float ks, vs;
   int cp[PP], ckb[PP], coff;  // the chunk's pages, their first keys, the first key's slot
+  int centry;                 // and its first entry
   bool whole;                 // every row of the chunk is a live key
 
   __device__ __forceinline__ void pages(const Q8AttendArgs& a, int e, int lane) {
@@ -240,18 +252,27 @@ struct Feeder {
       const int src = e - gbase + i;
       cp[i] = __shfl_sync(0xffffffffu, pid, src);
       ckb[i] = __shfl_sync(0xffffffffu, blk, src) * a.page + coff;
-      const float k = __shfl_sync(0xffffffffu, ks, src), v = __shfl_sync(0xffffffffu, vs, src);
       if (cp[i] < 0) ckb[i] = INT_MAX / 2;  // past every row
       some |= ckb[i] < u.hi && ckb[i] + w > u.lo;
       full &= ckb[i] >= full_lo && ckb[i] + w <= full_hi;
       whole &= ckb[i] >= u.lo && ckb[i] + w <= u.hi;
+      if (lane == 0) meta->kb[i] = ckb[i];
+    }
+    if (lane == 0) meta->state = some ? (full ? 2 : 1) : 0;
+    centry = e;
+  }
+
+  // Their scales: behind the copies, which do not need them.
+  __device__ __forceinline__ void scales(ChunkMeta<PP>* meta, int lane) {
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int src = centry - gbase + i;
+      const float k = __shfl_sync(0xffffffffu, ks, src), v = __shfl_sync(0xffffffffu, vs, src);
       if (lane == 0) {
         meta->ks[i] = k;
         meta->vs[i] = v;
-        meta->kb[i] = ckb[i];
       }
     }
-    if (lane == 0) meta->state = some ? (full ? 2 : 1) : 0;
   }
 
   // Copies K or V of the chunk into a slot.
@@ -320,8 +341,31 @@ struct Rows {
     return ((long)s.first + r / a.G) * a.Hq + h * a.G + r % a.G;
   }
 
-  __device__ __forceinline__ void load(const Q8AttendArgs& a, const Unit& u, int h, int lane) {
+  // The lane's components of its two query rows, as they are in memory.
+  struct Raw {
+    uint4 x[2][D / 32 * PARTS];
+  };
+  __device__ __forceinline__ void fetch(Raw& raw, const Q8AttendArgs& a, const Unit& u, int h,
+                                        int lane) {
     const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = u.r0 + g + 8 * i;
+      const bool real = r < u.s.n * a.G;
+      const T* src = static_cast<const T*>(a.q) + (real ? row_of(a, u.s, h, r) : 0) * D + 16 * t;
+      // components of step 4 half + j are 16 (4 half + t) + 4 j ..
+#pragma unroll
+      for (int c = 0; c < D / 32 * PARTS; ++c) {
+        const int half = c / (2 * PARTS), piece = c % (2 * PARTS);
+        raw.x[i][c] = real ? __ldg(reinterpret_cast<const uint4*>(src + 64 * half) + piece)
+                           : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void load(const Raw& raw, const Q8AttendArgs& a, const Unit& u,
+                                       int lane) {
+    const int g = lane >> 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = u.r0 + g + 8 * i;
@@ -329,19 +373,22 @@ struct Rows {
       const int pos = u.s.len - u.s.n + r / a.G;
       hi[i] = real && u.hi > 0 ? pos + 1 : 0;
       lo[i] = a.keys == q8::KEYS_WINDOW ? max(0, pos + 1 - a.window) : 0;
-      const T* src = static_cast<const T*>(a.q) + (real ? row_of(a, u.s, h, r) : 0) * D;
-      // lane t's components of step 4 half + j are 16 (4 half + t) + 4 j ..
       float x[D / 4];
-      float big = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        if (real) {
-          q8::Vec8<T>::load(src + 64 * (c >> 1) + 16 * t + 8 * (c & 1), x + 8 * c);
-        } else {
+      for (int c = 0; c < D / 32 * PARTS; ++c) {
+        const uint4 v = raw.x[i][c];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[8 * c + j] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          if (PARTS == 2) {
+            x[4 * c + k] = __uint_as_float(w[k]);
+          } else {
+            x[(8 * c + 2 * k) % (D / 4)] = __uint_as_float(w[k] << 16);
+            x[(8 * c + 2 * k + 1) % (D / 4)] = __uint_as_float(w[k] & 0xffff0000u);
+          }
         }
       }
+      float big = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 4; ++j)
         if (fabsf(x[j]) < INFINITY) big = fmaxf(big, fabsf(x[j]));
@@ -654,37 +701,64 @@ struct Rows {
     }
   }
 
-  __device__ __forceinline__ void store(float* part, const float (&lse2)[2], int lane) {
-    const int g = lane >> 2, t = lane & 3;
+  // A partial keeps the fragments' order: float4 32 j + lane is o[j] of the lane.
+  __device__ __forceinline__ void store(float* part, float* part_lse, const float (&lse2)[2],
+                                        int lane) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* dst = part + (g + 8 * i) * D + (D / 4) * t;
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int j = 0; j < NT; j += 4)
-          *reinterpret_cast<float4*>(dst + NT * c + j) =
-              make_float4(o[j][2 * i + c], o[j + 1][2 * i + c], o[j + 2][2 * i + c],
-                          o[j + 3][2 * i + c]);
-      if (t == 0) part[ROWS * D + g + 8 * i] = lse2[i];
+    for (int j = 0; j < NT; ++j)
+      reinterpret_cast<float4*>(part)[32 * j + lane] =
+          make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+    if ((lane & 3) == 0) {
+      part_lse[lane >> 2] = lse2[0];
+      part_lse[(lane >> 2) + 8] = lse2[1];
     }
   }
 };
 
+// Output tiles 4 jg .. 4 jg + 3 of fragment lane `lane` to the output's rows.
+template <typename T, int D>
+__device__ __forceinline__ void write_group(const Q8AttendArgs& a, const Seq& s, int h, int r0,
+                                            int jg, int lane, const float4 (&x)[4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + g + 8 * i;
+    if (r >= s.n * a.G) continue;
+    T* dst = static_cast<T*>(a.out) + Rows<T, D>::row_of(a, s, h, r) * D + (D / 4) * t + 4 * jg;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = i == 0 ? (c ? x[k].y : x[k].x) : (c ? x[k].w : x[k].z);
+      if (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(dst + D / 8 * c) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(dst + D / 8 * c) =
+            make_uint2(ptx::pack_bf16(v[0], v[1]), ptx::pack_bf16(v[2], v[3]));
+    }
+  }
+}
+
 // A warp's unfinished unit: begun before its share or continued behind it.
 struct Segment {
-  int tile, h;       // tile -1: none
+  long u0;            // its first chunk's place
+  int nc;             // its chunks; 0: no segment
+  int tile, h, r0, first, n;
   const float* part;
 };
+constexpr int kSegs = 2 * kWarps;
 
 template <typename T, int D, int PP>
 struct Smem {
   static constexpr int RING = kWarps * Geo<D>::RING;
   static constexpr int META = RING;
   static constexpr int SEGS = (META + kWarps * 2 * (int)sizeof(ChunkMeta<PP>) + 15) / 16 * 16;
-  static constexpr int SUMS = SEGS + 2 * kWarps * (int)sizeof(Segment);
+  static constexpr int LSE = SEGS + kSegs * (int)sizeof(Segment);  // of the segments' rows
+  static constexpr int WGT = LSE + kSegs * ROWS * 4;               // their weights in the join
+  static constexpr int SUMS = WGT + kSegs * ROWS * 4;
   static constexpr int PRE = SUMS + kWarps * 8;
-  static constexpr int BYTES = PRE + (kSmemTiles + 1) * 8;
+  static constexpr int LENS = PRE + (kSmemTiles + 1) * 8;
+  static constexpr int BYTES = LENS + kSmemTiles * 4;
 };
 
 // MULTI: a tile can hold several tokens, which see different keys.
@@ -695,6 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
+  float* seg_lse = reinterpret_cast<float*>(smem + S::LSE);
+  float* seg_wgt = reinterpret_cast<float*>(smem + S::WGT);
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
@@ -704,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pl.rt = a.rt;
   pl.tseq = nullptr;
   pl.tbase = nullptr;
+  pl.lens = nullptr;
   if (a.plan_pre) {
     pl.pre = a.plan_pre;
     pl.tseq = a.plan_seq;
@@ -712,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     long* pre = reinterpret_cast<long*>(smem + S::PRE);
     long* sums = reinterpret_cast<long*>(smem + S::SUMS);
+    int* lens = reinterpret_cast<int*>(smem + S::LENS);
     long base = 0;
     if (tid == 0) pre[0] = 0;
     for (int t0 = 0; t0 < a.tiles; t0 += kThreads) {
@@ -722,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Seq s = q8::sequence(a, b);
         if (!s.ok && blockIdx.x == 0) atomicOr(a.err, s.err);
         mine = (long)q8::chunks_of(a, s, (tile - b * a.rt) * ROWS, ROWS, CK) * a.Hkv;
+        lens[tile] = s.ok ? s.len : -1;
       }
       long run = mine;
 #pragma unroll
@@ -740,10 +819,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tile < a.tiles) pre[tile + 1] = before + run;
       __syncthreads();
     }
-    __syncthreads();
     pl.pre = pre;
+    pl.lens = lens;
   }
-  if (tid < 2 * kWarps) segs[tid].tile = -1;
+  if (tid < kSegs) segs[tid].nc = 0;
   __syncthreads();
   const long V = pl.tiles ? pl.pre[pl.tiles] : 0;
   // few chunks: fewer blocks, so that a block's warps share its merge
@@ -751,10 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int C = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
   const int cta = blockIdx.x;
   q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
-  if (cta >= C || V == 0) {
-    if (tid == 0) mm[cta].unit = -1;
-    return;
-  }
+  if (tid == 0) mm[cta].unit = -1;
+  if (cta >= C || V == 0) return;
   const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
   const long x0 = X0 + (X1 - X0) * warp / kWarps, x1 = X0 + (X1 - X0) * (warp + 1) / kWarps;
 
@@ -767,14 +844,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     feed.start(a, pl, x0);
     Place at = feed.at;
     Unit u = feed.u;
-    // K and V of the first chunk into slots 0 and 1
-    feed.look(a, meta, lane);
-    feed.template copy<false>(a, ring_u, lane);
-    ptx::cp_async_commit();
-    feed.template copy<true>(a, ring_u + TILE, lane);
-    ptx::cp_async_commit();
     Rows<T, D> rows;
-    rows.load(a, u, at.h, lane);
+    {
+      typename Rows<T, D>::Raw raw;
+      rows.fetch(raw, a, u, at.h, lane);
+      // K and V of the first chunk into slots 0 and 1
+      feed.look(a, meta, lane);
+      feed.template copy<false>(a, ring_u, lane);
+      ptx::cp_async_commit();
+      feed.template copy<true>(a, ring_u + TILE, lane);
+      ptx::cp_async_commit();
+      rows.load(raw, a, u, lane);
+      feed.scales(meta, lane);
+    }
     rows.clear();
     bool whole = at.c == 0;  // the unit's first chunk is the warp's
     int sk = 0;              // slot of the chunk's K; its V is in the next, the next K behind that
@@ -791,6 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         feed.template copy<false>(a, ring_u + sn * TILE, lane);
       }
       ptx::cp_async_commit();
+      if (more) feed.scales(meta + (mi ^ 1), lane);
       const ChunkMeta<PP>& sm = meta[mi];
       const int state = sm.state;
       float z[NS][4];
@@ -817,20 +900,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           rows.write(a, u, at.h, lse2, lane);
         } else if (more) {
           float* part = a.hold + ((long)cta * kWarps + warp) * Geo<D>::PART;
-          rows.store(part, lse2, lane);
-          if (lane == 0) segs[2 * warp] = Segment{at.tile, at.h, part};
+          rows.store(part, seg_lse + 2 * warp * ROWS, lse2, lane);
+          if (lane == 0)
+            segs[2 * warp] = Segment{x0 + x - at.c, at.nc, at.tile, at.h, u.r0, u.s.first, u.s.n, part};
         } else {
           ptx::cp_async_wait<0>();
           __syncwarp();  // the ring is free
           float* part = reinterpret_cast<float*>(ring);
-          rows.store(part, lse2, lane);
-          if (lane == 0) segs[2 * warp + 1] = Segment{at.tile, at.h, part};
+          rows.store(part, seg_lse + (2 * warp + 1) * ROWS, lse2, lane);
+          if (lane == 0)
+            segs[2 * warp + 1] =
+                Segment{x0 + x - at.c, at.nc, at.tile, at.h, u.r0, u.s.first, u.s.n, part};
         }
         if (more) {
           const int tile = at.tile;
           at.next(pl, a.Hkv);
           if (at.tile != tile) u.load(a, pl, at.tile);
-          rows.load(a, u, at.h, lane);
+          typename Rows<T, D>::Raw raw;
+          rows.fetch(raw, a, u, at.h, lane);
+          rows.load(raw, a, u, lane);
           rows.clear();
           whole = true;
         }
@@ -842,126 +930,173 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   // ---- join the block's segments of each unit ----
-  long head = -1;  // unit in the block's first slot
-  int from = 0;
-  for (int k = 0; k < 2 * kWarps;) {
-    const int tile = segs[k].tile, h = segs[k].h;
-    if (tile < 0) {
-      ++k;
-      continue;
-    }
-    int end = k + 1;  // segments k .. end - 1 (with gaps) are of one unit
-    for (int e = k + 1; e < 2 * kWarps; ++e) {
-      if (segs[e].tile < 0) continue;
-      if (segs[e].tile != tile || segs[e].h != h) break;
-      end = e + 1;
-    }
-    const int nc = (int)((pl.pre[tile + 1] - pl.pre[tile]) / a.Hkv);
-    const long u0 = pl.pre[tile] + (long)h * nc, u1 = u0 + nc;
-    const bool done = u0 >= X0 && u1 <= X1;
-    float* slot = a.part + (2l * cta + (u0 < X0 ? 0 : 1)) * Geo<D>::PART;
-    if (!done) {
-      if (u0 < X0) {
-        head = (long)tile * a.Hkv + h;
-        from = u1 <= X1 ? q8::block_of(u0, V, C) : -1;
-      }
-    }
-    Unit u;
-    if (done) u.load(a, pl, tile);
-#pragma unroll 2
-    for (int r = warp; r < ROWS; r += kWarps) {
-      float top = -INFINITY;
-      for (int e = k; e < end; ++e)
-        if (segs[e].tile >= 0) top = fmaxf(top, segs[e].part[ROWS * D + r]);
+  // Lane e of each warp holds segment e; the segments of one unit are a group,
+  // a bit mask, led by its lowest. Thread (e, r) weighs row r of segment e.
+  static_assert(kSegs * ROWS == kThreads, "a thread for each segment's row");
+  const Segment mine = segs[lane % kSegs];
+  const bool have = lane < kSegs && mine.nc > 0;
+  const unsigned group = __match_any_sync(0xffffffffu, have ? mine.u0 : -1l - lane);
+  unsigned leaders = __ballot_sync(0xffffffffu, have && (group & ((1u << lane) - 1)) == 0);
+  {
+    const int e = tid / ROWS, r = tid % ROWS;
+    const unsigned set = __shfl_sync(0xffffffffu, have ? group : 0u, e);
+    if (set) {
+      float top = -INFINITY, sum = 0.f;
+      for (unsigned m = set; m; m &= m - 1) top = fmaxf(top, seg_lse[(__ffs(m) - 1) * ROWS + r]);
       const float base = top == -INFINITY ? 0.f : top;
-      float acc[D / 32], sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-      for (int e = k; e < end; ++e) {
-        if (segs[e].tile < 0) continue;
-        const float* p = segs[e].part;
-        const float wgt = ptx::ex2(p[ROWS * D + r] - base);
-        sum += wgt;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] += wgt * p[r * D + i * 32 + lane];
-      }
-      const float f = sum == 0.f ? 0.f : 1.f / sum;
-      const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-      if (!done) {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) slot[r * D + i * 32 + lane] = acc[i] * f;
-        if (lane == 0) slot[ROWS * D + r] = lse2;
-      } else if (u.r0 + r < u.s.n * a.G) {
-        const long row = Rows<T, D>::row_of(a, u.s, h, u.r0 + r);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          static_cast<T*>(a.out)[row * D + i * 32 + lane] = from_f32<T>(acc[i] * f);
-        if (lane == 0 && a.lse) a.lse[row] = lse2 * q8::kLn2;
+      for (unsigned m = set; m; m &= m - 1)
+        sum += ptx::ex2(seg_lse[(__ffs(m) - 1) * ROWS + r] - base);
+      seg_wgt[tid] = sum == 0.f ? 0.f : ptx::ex2(seg_lse[tid] - base) / sum;
+      if (__ffs(set) - 1 == e) {
+        const Segment& sg = segs[e];
+        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+        const Seq s{sg.first, sg.n, 0, true, 0u};
+        if (sg.u0 >= X0 && sg.u0 + sg.nc <= X1) {
+          if (sg.r0 + r < sg.n * a.G && a.lse)
+            a.lse[Rows<T, D>::row_of(a, s, sg.h, sg.r0 + r)] = lse2 * q8::kLn2;
+        } else {
+          a.part[(2l * cta + (sg.u0 < X0 ? 0 : 1)) * Geo<D>::PART + ROWS * D + r] = lse2;
+          if (r == 0 && sg.u0 < X0 && sg.u0 + sg.nc <= X1) {
+            mm[cta].unit = (long)sg.tile * a.Hkv + sg.h;
+            mm[cta].from = q8::block_of(sg.u0, V, C);
+          }
+        }
       }
     }
-    k = end;
   }
-  if (tid == 0) {
-    mm[cta].unit = head >= 0 && from >= 0 ? head : -1;
-    mm[cta].from = from;
+  __syncthreads();
+  // four warps (two for d = 64) join a group, a lane four output tiles of its fragment
+  constexpr int JG = D / 32;
+  const int jg = warp % JG, g = lane >> 2;
+  for (int k = 0; leaders; leaders &= leaders - 1, ++k) {
+    if (k % (kWarps / JG) != warp / JG) continue;
+    const int lead = __ffs(leaders) - 1;
+    const unsigned set = __shfl_sync(0xffffffffu, group, lead);
+    float4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (unsigned m = set; m; m &= m - 1) {
+      const int e = __ffs(m) - 1;
+      const float4* part = reinterpret_cast<const float4*>(segs[e].part) + 128 * jg + lane;
+      const float w0 = seg_wgt[e * ROWS + g], w1 = seg_wgt[e * ROWS + g + 8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = part[32 * j];
+        acc[j].x = fmaf(w0, x.x, acc[j].x);
+        acc[j].y = fmaf(w0, x.y, acc[j].y);
+        acc[j].z = fmaf(w1, x.z, acc[j].z);
+        acc[j].w = fmaf(w1, x.w, acc[j].w);
+      }
+    }
+    const Segment& sg = segs[lead];
+    if (sg.u0 >= X0 && sg.u0 + sg.nc <= X1) {
+      const Seq s{sg.first, sg.n, 0, true, 0u};
+      write_group<T, D>(a, s, sg.h, sg.r0, jg, lane, acc);
+    } else {
+      float4* slot = reinterpret_cast<float4*>(
+          a.part + (2l * cta + (sg.u0 < X0 ? 0 : 1)) * Geo<D>::PART) + 128 * jg + lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) slot[32 * j] = acc[j];
+    }
   }
 }
 
-// Joins the partials of a unit that lies in several blocks: block (c, r) does
-// row r of the unit that ends in attention block c, from slot 2 f + 1 of the
-// block f it begins in and slots 2 i of the blocks behind it up to c.
+// Joins the partials of a unit that lies in several blocks: block (c, jg) does
+// output tiles 4 jg .. of the unit that ends in attention block c, from slot
+// 2 f + 1 of the block f it begins in and slots 2 i of the blocks behind it up
+// to c. Its warps take every kMergeWarps-th partial.
+constexpr int kMergeWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) q8_merge_kernel(const Q8AttendArgs a, int tile_rows) {
-  constexpr int V = D / 32;
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    q8_merge_kernel(const __grid_constant__ Q8AttendArgs a) {
   ptx::grid_dep_wait();
   const q8::MergeMeta mm = reinterpret_cast<const q8::MergeMeta*>(a.meta)[blockIdx.x];
   if (mm.unit < 0) return;
-  const int tile = (int)(mm.unit / a.Hkv), h = (int)(mm.unit % a.Hkv), r = blockIdx.y;
-  const int b = a.plan_pre ? a.plan_seq[tile] : tile / a.rt;
-  const int r0 = (tile - (a.plan_pre ? a.plan_base[b] : b * a.rt)) * tile_rows;
-  const Seq s = q8::sequence(a, b);
-  if (r0 + r >= s.n * a.G) return;
-  const long stride = (long)tile_rows * (D + 1);
+  __shared__ float s_top[kMergeWarps][ROWS], s_sum[kMergeWarps][ROWS];
+  __shared__ float4 s_acc[kMergeWarps][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, jg = blockIdx.y;
+  const int g = lane >> 2, t = lane & 3;
   const int n = (int)blockIdx.x - mm.from + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto part = [&](int i) { return a.part + (2l * (mm.from + i) + (i == 0 ? 1 : 0)) * stride; };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[tile_rows * D + r]);
-  top = warp_max(top);
-  const float base = top == -INFINITY ? 0.f : top;
-  float acc[V], sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  auto part = [&](int i) { return a.part + (2l * (mm.from + i) + (i == 0 ? 1 : 0)) * Geo<D>::PART; };
+  float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll 4
-  for (int i = warp; i < n; i += 4) {
+  for (int i = 4 * warp + t; i < n; i += 4 * kMergeWarps) {
+    const float* l = part(i) + ROWS * D;
+    top[0] = fmaxf(top[0], l[g]);
+    top[1] = fmaxf(top[1], l[g + 8]);
+  }
+  top[0] = quad_max(top[0]);
+  top[1] = quad_max(top[1]);
+  if (t == 0) {
+    s_top[warp][g] = top[0];
+    s_top[warp][g + 8] = top[1];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    top[0] = fmaxf(top[0], s_top[w][g]);
+    top[1] = fmaxf(top[1], s_top[w][g + 8]);
+  }
+  const float b0 = top[0] == -INFINITY ? 0.f : top[0], b1 = top[1] == -INFINITY ? 0.f : top[1];
+  float4 acc[4];
+  float sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = warp; i < n; i += kMergeWarps) {
     const float* p = part(i);
-    const float w = ptx::ex2(p[tile_rows * D + r] - base);
-    sum += w;
-    if (V == 4) {
-      const float4 x = reinterpret_cast<const float4*>(p + r * D)[lane];
-      acc[0] += w * x.x;
-      acc[1] += w * x.y;
-      acc[V - 2] += w * x.z;
-      acc[V - 1] += w * x.w;
-    } else {
-      const float2 x = reinterpret_cast<const float2*>(p + r * D)[lane];
-      acc[0] += w * x.x;
-      acc[1] += w * x.y;
+    const float w0 = ptx::ex2(p[ROWS * D + g] - b0), w1 = ptx::ex2(p[ROWS * D + g + 8] - b1);
+    sum[0] += w0;
+    sum[1] += w1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(p)[128 * jg + 32 * j + lane];
+      acc[j].x = fmaf(w0, x.x, acc[j].x);
+      acc[j].y = fmaf(w0, x.y, acc[j].y);
+      acc[j].z = fmaf(w1, x.z, acc[j].z);
+      acc[j].w = fmaf(w1, x.w, acc[j].w);
     }
   }
-  __shared__ float s_acc[4][D], s_sum[4];
 #pragma unroll
-  for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  const int dim = threadIdx.x;
-  const float all = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-  const long row = Rows<T, D>::row_of(a, s, h, r0 + r);
-  if (dim < D) {
-    const float v = s_acc[0][dim] + s_acc[1][dim] + s_acc[2][dim] + s_acc[3][dim];
-    static_cast<T*>(a.out)[row * D + dim] = from_f32<T>(all == 0.f ? 0.f : v / all);
+  for (int j = 0; j < 4; ++j) s_acc[warp][j][lane] = acc[j];
+  if (t == 0) {
+    s_sum[warp][g] = sum[0];
+    s_sum[warp][g + 8] = sum[1];
   }
-  if (dim == 0 && a.lse) a.lse[row] = all == 0.f ? -INFINITY : (top + log2f(all)) * q8::kLn2;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    sum[0] += s_sum[w][g];
+    sum[1] += s_sum[w][g + 8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = s_acc[w][j][lane];
+      acc[j].x += x.x;
+      acc[j].y += x.y;
+      acc[j].z += x.z;
+      acc[j].w += x.w;
+    }
+  }
+  const float f0 = sum[0] == 0.f ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f ? 0.f : 1.f / sum[1];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = make_float4(acc[j].x * f0, acc[j].y * f0, acc[j].z * f1, acc[j].w * f1);
+  const int tile = (int)(mm.unit / a.Hkv), h = (int)(mm.unit % a.Hkv);
+  const int b = a.plan_pre ? a.plan_seq[tile] : tile / a.rt;
+  const int r0 = (tile - (a.plan_pre ? a.plan_base[b] : b * a.rt)) * ROWS;
+  Seq s{b, 1, 0, true, 0u};
+  if (a.cu) q8::token_range(a.cu, b, a.N, s.first, s.n);
+  write_group<T, D>(a, s, h, r0, jg, lane, acc);
+  if (jg == 0 && t == 0 && a.lse) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + g + 8 * i;
+      if (r < s.n * a.G)
+        a.lse[Rows<T, D>::row_of(a, s, h, r)] =
+            sum[i] == 0.f ? -INFINITY : (top[i] + log2f(sum[i])) * q8::kLn2;
+    }
+  }
 }
 
 // The plan of a call with offsets, or of more tiles than a block takes in: the
@@ -1059,7 +1194,8 @@ cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
       return e;
   }
   TraceScope trace("q8_merge", stream);
-  return launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, ROWS), dim3(128), 0, stream, a, ROWS);
+  return launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, D / 32), dim3(32 * kMergeWarps), 0, stream,
+                    a);
 }
 
 template <typename T, int D>
