@@ -200,6 +200,13 @@ struct Q8AttendArgs {
   int* plan_base;
   int tiles, rt, blocks, min_chunks;
 };
+// Chunks of queries on the tensor memory (q8_prefill_tc.cu): bf16, d = 128,
+// pages of 32 tokens or more. The plan is made by the caller, for tiles of
+// kQ8TcRows rows and chunks of kQ8TcKeys keys.
+constexpr int kQ8TcRows = 256, kQ8TcKeys = 128;
+bool q8_prefill_tc_shape(const nsa_params& p);
+size_t q8_prefill_tc_part_bytes();
+cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, cudaStream_t stream);
 size_t q8_attend_ws_bytes(const nsa_params& p, bool ragged);
 cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cudaStream_t stream);
 

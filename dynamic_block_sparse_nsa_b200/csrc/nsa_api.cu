@@ -189,7 +189,7 @@ Q8AttendArgs q8_attend_args(const nsa_params* p, const nsa_q8_cache* c, int keys
   a.num_pages = c->num_pages;
   a.max_pages = (p->T + p->sel_block - 1) / p->sel_block;
   a.keys = keys;
-  a.window = p->window;
+  a.window = p->window < p->T ? p->window : p->T;
   a.n = p->top_n;
   a.scale_log2 = eff_scale(p) * 1.4426950408889634f;
   return a;

@@ -29,13 +29,14 @@
 // the same way in q) or the same 16 components of four keys (V), so no
 // transposition is needed; the slots' swizzles make both conflict-free.
 #include <algorithm>
-#include <utility>
 
 #include "q8_attend.cuh"
 
 namespace nsa {
 namespace {
 
+using q8::Place;
+using q8::Plan;
 using q8::Seq;
 
 constexpr int kWarps = 8;
@@ -116,46 +117,6 @@ __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
-
-// Where the plan's prefix lives and how a tile maps to its sequence.
-struct Plan {
-  const long* pre;   // chunks (times KV heads) before each tile, [tiles + 1]
-  const int* tseq;   // sequence of each tile; null: tile / rt
-  const int* tbase;  // first tile of each sequence (with tseq)
-  const int* lens;   // without tseq: length of each tile's sequence; -1: a bad one
-  int tiles, rt;
-};
-
-// A place in the list of chunks: (tile, KV head, chunk).
-struct Place {
-  int tile, h, c, nc;
-  __device__ __forceinline__ void init(const Plan& pl, int hkv, long x) {
-    int lo = 0, hi = pl.tiles - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pl.pre[mid] <= x)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    tile = lo;
-    nc = (int)((pl.pre[lo + 1] - pl.pre[lo]) / hkv);
-    const int r = (int)(x - pl.pre[lo]);
-    h = r / nc;
-    c = r - h * nc;
-  }
-  // Next chunk; true when it belongs to another unit.
-  __device__ __forceinline__ bool next(const Plan& pl, int hkv) {
-    if (++c < nc) return false;
-    c = 0;
-    if (++h == hkv) {
-      h = 0;
-      ++tile;
-      if (tile < pl.tiles) nc = (int)((pl.pre[tile + 1] - pl.pre[tile]) / hkv);
-    }
-    return true;
-  }
-};
 
 // A unit's sequence and row range.
 struct Unit {
@@ -1127,6 +1088,7 @@ __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArg
                                                                int chunk) {
   __shared__ long sums[kPlanThreads / 32];
   ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   const int tid = threadIdx.x;
   long base = 0, all;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
@@ -1138,11 +1100,7 @@ __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArg
       mine = q8::tiles_of(a, s.n, tile_rows);
     }
     const long at = block_scan(mine, sums, all);
-    if (b < a.B) {
-      a.plan_base[b] = (int)(base + at);
-      for (long k = 0; k < mine; ++k)
-        if (base + at + k < a.tiles) a.plan_seq[base + at + k] = b;
-    }
+    if (b < a.B) a.plan_base[b] = (int)(base + at);
     base += all;
   }
   const int tiles = (int)(base < a.tiles ? base : a.tiles);
@@ -1156,7 +1114,15 @@ __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArg
     const int t = t0 + tid;
     long mine = 0;
     if (t < tiles) {
-      const int b = a.plan_seq[t];
+      int b = 0, last = a.B - 1;  // the last sequence that begins at or before tile t
+      while (b < last) {
+        const int mid = (b + last + 1) >> 1;
+        if (a.plan_base[mid] <= t)
+          b = mid;
+        else
+          last = mid - 1;
+      }
+      a.plan_seq[t] = b;
       const Seq s = q8::sequence(a, b);
       mine = (long)q8::chunks_of(a, s, (t - a.plan_base[b]) * tile_rows, tile_rows, chunk) * a.Hkv;
     }
@@ -1164,22 +1130,6 @@ __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArg
     if (t < tiles) a.plan_pre[t + 1] = base + at + mine;
     base += all;
   }
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 template <typename T, int D, int PP>
@@ -1190,11 +1140,11 @@ cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
   if ((e = ensure_dyn_smem((const void*)kern, smem)) != cudaSuccess) return e;
   {
     TraceScope trace("q8_attend", stream);
-    if ((e = launch_pdl(kern, dim3(a.blocks), dim3(kThreads), smem, stream, a)) != cudaSuccess)
+    if ((e = q8::launch_pdl(kern, dim3(a.blocks), dim3(kThreads), smem, stream, a)) != cudaSuccess)
       return e;
   }
   TraceScope trace("q8_merge", stream);
-  return launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, D / 32), dim3(32 * kMergeWarps), 0, stream,
+  return q8::launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, D / 32), dim3(32 * kMergeWarps), 0, stream,
                     a);
 }
 
@@ -1227,7 +1177,8 @@ Layout layout(const nsa_params& p, bool ragged) {
     return o;
   };
   const size_t part = (size_t)(ROWS * p.d + ROWS) * 4;
-  L.part = take(part * 2 * kQ8MaxBlocks);
+  const size_t tc = ragged && q8_prefill_tc_shape(p) ? q8_prefill_tc_part_bytes() : 0;
+  L.part = take(std::max(part * 2 * kQ8MaxBlocks, tc));
   L.hold = take(part * kWarps * kQ8MaxBlocks);
   L.meta = take(sizeof(q8::MergeMeta) * kQ8MaxBlocks);
   const long tiles = most_tiles(p, ragged, (long)p.B * p.T);
@@ -1260,15 +1211,21 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
   a.plan_pre = nullptr;
   a.plan_seq = nullptr;
   a.plan_base = nullptr;
+  // Chunks of queries on the tensor-memory kernel once a sequence has rows to
+  // fill a good part of its 128-row tiles with; below that most of the tile is
+  // padding, and the kernel here reads the same codes once per 16 rows.
+  const bool tc = ragged && q8_prefill_tc_shape(p) && (long)a.N * a.G >= 32l * p.B;
+  if (tc) a.tiles = (int)((long)a.N * a.G / kQ8TcRows + p.B);
   if (ragged || a.tiles > kSmemTiles) {
     a.plan_pre = reinterpret_cast<long*>(w + L.pre);
     a.plan_seq = reinterpret_cast<int*>(w + L.seq);
     a.plan_base = reinterpret_cast<int*>(w + L.base);
     TraceScope trace("q8_plan", stream);
-    const cudaError_t e = launch_pdl(q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a,
-                                     ROWS, CK);
+    const cudaError_t e = q8::launch_pdl(q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a,
+                                         tc ? kQ8TcRows : ROWS, tc ? kQ8TcKeys : CK);
     if (e != cudaSuccess) return e;
   }
+  if (tc) return launch_q8_prefill_tc(a, stream);
   const bool bf16 = p.dtype == NSA_DTYPE_BF16;
   using bf = __nv_bfloat16;
   if (p.d == 128) return bf16 ? launch<bf, 128>(a, stream) : launch<float, 128>(a, stream);

@@ -12,6 +12,7 @@
 #pragma once
 
 #include <climits>
+#include <utility>
 
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -84,12 +85,70 @@ __device__ __forceinline__ int block_of(long x, long V, int C) {
   return c;
 }
 
+// Where the plan's prefix lives and how a tile maps to its sequence.
+struct Plan {
+  const long* pre;   // chunks (times KV heads) before each tile, [tiles + 1]
+  const int* tseq;   // sequence of each tile; null: tile / rt
+  const int* tbase;  // first tile of each sequence (with tseq)
+  const int* lens;   // without tseq: length of each tile's sequence; -1: a bad one
+  int tiles, rt;
+};
+
+// A place in the list of chunks: (tile, KV head, chunk).
+struct Place {
+  int tile, h, c, nc;
+  __device__ __forceinline__ void init(const Plan& pl, int hkv, long x) {
+    int lo = 0, hi = pl.tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pl.pre[mid] <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    tile = lo;
+    nc = (int)((pl.pre[lo + 1] - pl.pre[lo]) / hkv);
+    const int r = (int)(x - pl.pre[lo]);
+    h = r / nc;
+    c = r - h * nc;
+  }
+  // Next chunk; true when it belongs to another unit.
+  __device__ __forceinline__ bool next(const Plan& pl, int hkv) {
+    if (++c < nc) return false;
+    c = 0;
+    if (++h == hkv) {
+      h = 0;
+      ++tile;
+      if (tile < pl.tiles) nc = (int)((pl.pre[tile + 1] - pl.pre[tile]) / hkv);
+    }
+    return true;
+  }
+};
+
 // Per block: the unit of slot 2 c when that unit ends in the block (else -1),
 // and the block it begins in.
 struct MergeMeta {
   long unit;
   int from, pad;
 };
+
+// Launches so that the grid may be scheduled while its predecessor in the
+// stream drains; every kernel here waits (grid_dep_wait) before it reads.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
 
 }  // namespace q8
 }  // namespace nsa

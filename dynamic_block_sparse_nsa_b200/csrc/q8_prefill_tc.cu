@@ -1,0 +1,742 @@
+// nsa_prefill_q8 on the sm_100a tensor memory: chunks of queries over the 8-bit
+// paged cache, bf16, d = 128, pages of 32 tokens or more. The mathematics is
+// that of q8_attend.cu (fp16 products with exact codes, a row scale for q, the
+// running maximum m and the output's own reference M); the work plan too, with
+// tiles of 256 query rows and chunks of 128 keys.
+//
+// 4 d flops a row and key make it a matrix kernel: per chunk and tile
+// S = Q K^T and O += P V, two 128-row halves each, S (later P) and O of both
+// halves in the 512 columns of tensor memory. Roles, one persistent block per
+// SM:
+//   warps 0-3, 4-7   softmax of a half, a thread per row: S from tensor memory,
+//                    P back over it, O rescaled when its reference moves by
+//                    more than 2^5, the epilogue;
+//   warps 8-11       codes from global memory to fp16 K and V tiles in shared
+//                    memory (128-byte swizzle), two buffers each, the next
+//                    tile's codes in flight in registers meanwhile;
+//   warp 12          issues the MMAs: while one half's softmax runs, the other
+//                    half's products do.
+// The bound is the softmax: an exponential for every score (16 a clock and SM)
+// takes as long as the two products of it.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "q8_attend.cuh"
+#include "tcgen05.cuh"
+
+namespace nsa {
+namespace {
+
+using q8::Place;
+using q8::Plan;
+using q8::Seq;
+
+constexpr int D = 128;
+constexpr int ROWS = kQ8TcRows;
+constexpr int CK = kQ8TcKeys;
+constexpr uint32_t ATOM = 16384;   // 128 rows x 64 halves
+constexpr uint32_t TILE = 32768;   // 128 rows x 128 halves
+constexpr int kThreads = 13 * 32;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kNegInf = 0xff800000u;
+constexpr float kLag = 5.f;        // how far M may fall behind before O is rescaled
+constexpr int kNanSlots = 4;       // units whose NaN marks are under way
+constexpr long kPart = (long)ROWS * D + ROWS;  // floats of a partial: o, lse2
+
+// Tensor-memory columns of half t: S, later P; and O.
+__device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
+__device__ __forceinline__ uint32_t o_col(int t) { return 256u + 128u * t; }
+
+struct Bars {
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t fin;
+  int abort;
+  uint32_t tmem;
+  int nan_flag[kNanSlots];
+};
+
+struct Smem {
+  unsigned char q[2][TILE];
+  unsigned char k[2][TILE];
+  unsigned char v[2][TILE];
+  Bars bars;
+  uint32_t nan_rows[kNanSlots][D][8];  // per component: the tile's tokens that see a NaN value
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                     unsigned* err) {
+  if (*abort) return false;
+  if (ptx::mbar_wait(bar, parity & 1u, kWaitNs)) return true;
+  atomicOr(err, kErrTimeout);
+  *abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ uint64_t kmaj(uint32_t base, int ks) {
+  return tc::sdesc(base + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024, tc::kSw128);
+}
+__device__ __forceinline__ uint64_t mnmaj(uint32_t base, int ks) {
+  return tc::sdesc(base + ks * 2048, ATOM, 1024, tc::kSw128);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float warp_min(float x) { return -warp_max(-x); }
+
+// A unit: a tile's rows of one KV head.
+struct Unit {
+  Seq s;
+  int b, r0, lo, hi, rows;
+  __device__ __forceinline__ void load(const Q8AttendArgs& a, const Plan& pl, int tile) {
+    b = pl.tseq[tile];
+    r0 = (tile - pl.tbase[b]) * ROWS;
+    s = q8::sequence(a, b);
+    rows = min(ROWS, s.n * a.G - r0);
+    q8::key_span(a, s, r0, ROWS, lo, hi);
+  }
+};
+
+// The block's chunks, unit by unit: `n` chunks of the current unit from `at.c` on.
+struct Walk {
+  Place at;
+  Unit u;
+  long x, end;
+  int n, seg;
+  __device__ __forceinline__ void start(const Q8AttendArgs& a, const Plan& pl, long x0, long x1) {
+    x = x0;
+    end = x1;
+    seg = 0;
+    at.init(pl, a.Hkv, x0);
+    u.load(a, pl, at.tile);
+    n = (int)min((long)(at.nc - at.c), x1 - x0);
+  }
+  __device__ __forceinline__ bool done() const { return x >= end; }
+  __device__ __forceinline__ void next(const Q8AttendArgs& a, const Plan& pl) {
+    x += n;
+    ++seg;
+    if (x >= end) return;
+    const int tile = at.tile;
+    at.c = at.nc - 1;  // (only a unit's last segment is followed by another)
+    at.next(pl, a.Hkv);
+    if (at.tile != tile) u.load(a, pl, at.tile);
+    n = (int)min((long)at.nc, end - x);
+  }
+  __device__ __forceinline__ int key0(int i) const { return (u.lo / CK + at.c + i) * CK; }
+};
+
+// Lane j's page of the chunk that begins at key0 (j < 128 / page); -1: none,
+// INT_MAX: not a page number.
+__device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int key0, int lane) {
+  const int first = key0 + lane * a.page;
+  if (lane * a.page >= CK || first >= u.hi) return -1;
+  const int pid = a.table[(long)u.b * a.max_pages + first / a.page];
+  return pid < 0 ? INT_MAX : pid;
+}
+
+// ---- codes to fp16 tiles ------------------------------------------------------
+
+struct Converter {
+  const Q8AttendArgs& a;
+  int warp, lane;  // of the four
+  __device__ __forceinline__ int row(int k) const { return 16 * k + 4 * warp + (lane >> 3); }
+
+  __device__ __forceinline__ void load(uint4 (&x)[8], const uint8_t* pages, const Unit& u, int h,
+                                       int key0, int pid) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = row(k), p = __shfl_sync(0xffffffffu, pid, 16 * k / a.page);
+      const int pos = key0 + r;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (p >= 0 && pos >= u.lo && pos < u.hi)
+        x[k] = __ldg(reinterpret_cast<const uint4*>(
+            pages + (((long)p * a.Hkv + h) * a.page + (r & (a.page - 1))) * D + (lane & 7) * 16));
+    }
+  }
+
+  // Row r's 16 components as two 16-byte pieces of the swizzled tile; lanes of
+  // the second half store theirs in the other order, so that the eight lanes
+  // of a row cover all banks.
+  __device__ __forceinline__ void store(const uint4 (&x)[8], unsigned char* tile) const {
+    const int c8 = lane & 7;
+    const bool odd = c8 >= 4;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = row(k);
+      unsigned char* dst = tile + (c8 >> 2) * ATOM + r * 128;
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      uint32_t hx[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hx[2 * i] = q8::e4m3x2_to_half2((uint16_t)(w[i] & 0xffffu));
+        hx[2 * i + 1] = q8::e4m3x2_to_half2((uint16_t)(w[i] >> 16));
+      }
+      const uint4 p0 = make_uint4(hx[0], hx[1], hx[2], hx[3]);
+      const uint4 p1 = make_uint4(hx[4], hx[5], hx[6], hx[7]);
+      const int c = (c8 & 3) * 2;
+      *reinterpret_cast<uint4*>(dst + (((c + odd) ^ (r & 7)) << 4)) = odd ? p1 : p0;
+      *reinterpret_cast<uint4*>(dst + (((c + !odd) ^ (r & 7)) << 4)) = odd ? p0 : p1;
+    }
+  }
+
+  // NaN values of keys that only some of the tile's tokens see: marked for
+  // those, and replaced by zeros (0 * NaN would reach the others).
+  __device__ void mark_nan(uint4 (&x)[8], const Unit& u, int key0, uint32_t (*marks)[8],
+                           int* flag) const {
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) found |= __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    }
+    if (!found) return;
+    const int tok0 = u.r0 / a.G, tok1 = (u.r0 + u.rows - 1) / a.G;
+    const int at0 = u.s.len - u.s.n + tok0;  // position of the tile's first token
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      const int key = key0 + row(k);
+      const int from = max(0, key - at0);
+      const int to = a.keys == q8::KEYS_WINDOW ? min(tok1 - tok0, key - at0 + a.window - 1)
+                                               : tok1 - tok0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t bad = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (!bad) continue;
+        w[i] &= ~bad;
+        for (int y = 0; y < 4; ++y)
+          if (bad >> (8 * y) & 1u)
+            for (int t = from; t <= to; ++t)
+              atomicOr(&marks[(lane & 7) * 16 + 4 * i + y][t >> 5], 1u << (t & 31));
+      }
+      x[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *flag = 1;
+    __threadfence_block();
+  }
+
+  __device__ void run(const Plan& pl, long X0, long X1, Smem& sm) const {
+    Bars& B = sm.bars;
+    volatile int* abort = &B.abort;
+    Walk w;
+    w.start(a, pl, X0, X1);
+    int i = 0;  // chunk of the segment
+    int key0 = w.key0(0), h = w.at.h, slot = 0;
+    Unit u = w.u;
+    int pid = check(page_of(a, u, key0, lane));
+    uint4 kx[8], vx[8];
+    load(kx, a.k_pages, u, h, key0, pid);
+    const int len = (int)(X1 - X0);
+    for (int j = 0; j < len; ++j) {
+      const int buf = j & 1;
+      load(vx, a.v_pages, u, h, key0, pid);
+      // the next chunk's pages
+      const Unit un = u;
+      const int kn = key0, sn = slot;
+      const bool more = j + 1 < len;
+      if (more) {
+        if (++i == w.n) {
+          w.next(a, pl);
+          i = 0;
+          u = w.u;
+          h = w.at.h;
+          slot = w.seg % kNanSlots;
+        }
+        key0 = w.key0(i);
+        pid = page_of(a, u, key0, lane);
+      }
+      if (j >= 2) wait(&B.k_empty[buf], (j >> 1) - 1, abort, a.err);
+      store(kx, sm.k[buf]);
+      ptx::fence_proxy_async();
+      ptx::mbar_arrive(&B.k_full[buf]);
+      if (more) {
+        pid = check(pid);
+        load(kx, a.k_pages, u, h, key0, pid);
+      }
+      if (edge(un, kn)) mark_nan(vx, un, kn, sm.nan_rows[sn], &B.nan_flag[sn]);
+      if (j >= 2) wait(&B.v_empty[buf], (j >> 1) - 1, abort, a.err);
+      store(vx, sm.v[buf]);
+      ptx::fence_proxy_async();
+      ptx::mbar_arrive(&B.v_full[buf]);
+    }
+  }
+
+  // Whether some token of the tile does not see all of the chunk.
+  __device__ __forceinline__ bool edge(const Unit& u, int key0) const {
+    const int tok0 = u.r0 / a.G, tok1 = (u.r0 + u.rows - 1) / a.G;
+    const int at0 = u.s.len - u.s.n;
+    return key0 + CK > at0 + tok0 + 1 ||
+           (a.keys == q8::KEYS_WINDOW && key0 < at0 + tok1 + 1 - a.window);
+  }
+
+  __device__ __forceinline__ int check(int pid) const {
+    if (pid >= a.num_pages) {
+      atomicOr(a.err, kErrPage);
+      return -1;
+    }
+    return pid;
+  }
+};
+
+// ---- MMAs (one thread) ----------------------------------------------------------
+
+__device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long X1, Smem& sm) {
+  Bars& B = sm.bars;
+  volatile int* abort = &B.abort;
+  const uint32_t tmem = B.tmem;
+  constexpr uint32_t iqk = tc::idesc_f16(128, 128, false, false);
+  constexpr uint32_t ipv = tc::idesc_f16(128, 128, false, true);
+  const uint32_t q0 = ptx::smem_u32(sm.q), k0 = ptx::smem_u32(sm.k), v0 = ptx::smem_u32(sm.v);
+  int segs[2] = {0, 0}, tiles[2] = {0, 0};  // per half: units begun, P tiles taken
+  Walk w;
+  bool ok = true;
+  int j = 0;  // the block's chunk
+  for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
+    const int halves = w.u.rows > 128 ? 2 : 1;
+    auto qk = [&](int t, int jj) {
+      const uint32_t kb = k0 + (jj & 1) * TILE;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        tc::mma_ss(tmem + s_col(t), kmaj(q0 + t * TILE, ks), kmaj(kb, ks), iqk, ks > 0);
+      if (t == halves - 1) tc::commit(&B.k_empty[jj & 1]);
+      tc::commit(&B.s_full[t]);
+    };
+    for (int t = 0; t < halves; ++t) ok = ok && wait(&B.q_full[t], segs[t]++, abort, a.err);
+    ok = ok && wait(&B.k_full[j & 1], j >> 1, abort, a.err);
+    if (!ok) break;
+    tc::fence_after_sync();
+    for (int t = 0; t < halves; ++t) qk(t, j);
+    for (int i = 0; ok && i < w.n; ++i, ++j) {
+      const bool more = i + 1 < w.n;
+      ok = wait(&B.v_full[j & 1], j >> 1, abort, a.err);
+      for (int t = 0; ok && t < halves; ++t) {
+        ok = wait(&B.p_full[t], tiles[t]++, abort, a.err);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t vb = v0 + (j & 1) * TILE;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mnmaj(vb, ks), ipv, (i > 0 || ks > 0));
+        if (t == halves - 1) tc::commit(&B.v_empty[j & 1]);
+        if (!more) tc::commit(&B.o_full[t]);
+        if (more) {
+          if (t == 0) {
+            ok = wait(&B.k_full[(j + 1) & 1], (j + 1) >> 1, abort, a.err);
+            tc::fence_after_sync();
+          }
+          if (ok) qk(t, j + 1);
+        }
+      }
+    }
+  }
+  tc::commit(&B.fin);
+  if (!ptx::mbar_wait(&B.fin, 0, kWaitNs)) atomicOr(a.err, kErrTimeout);
+}
+
+// ---- softmax (a thread per row of half t) -----------------------------------------
+
+struct Softmax {
+  const Q8AttendArgs& a;
+  Smem& sm;
+  int t, row;      // half, row of it
+  uint32_t tl;     // the warp's lanes of tensor memory
+  float qf;        // row factor of the scores
+  int lo, hi;      // keys the row sees
+
+  // The row's query, scaled into fp16's range, into the half's tile.
+  __device__ __forceinline__ void load_query(const Unit& u, int h) {
+    const int r = u.r0 + 128 * t + row;
+    const bool real = r < u.s.n * a.G;
+    const int pos = u.s.len - u.s.n + r / a.G;
+    hi = real && u.hi > 0 ? pos + 1 : 0;
+    lo = a.keys == q8::KEYS_WINDOW ? max(0, pos + 1 - a.window) : 0;
+    uint4 x[16];
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.q) + (real ? out_row(u, h, r) : 0) * D);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) x[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    float big = 0.f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f0 = fabsf(__uint_as_float(w[i] << 16));
+        const float f1 = fabsf(__uint_as_float(w[i] & 0xffff0000u));
+        if (f0 < INFINITY) big = fmaxf(big, f0);
+        if (f1 < INFINITY) big = fmaxf(big, f1);
+      }
+    }
+    // 2^up brings the largest component to [2^14, 2^15)
+    int up = big > 0.f ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
+    up = min(max(up, -120), 120);
+    // (a negative softmax scale's sign goes into q)
+    const float mul = a.scale_log2 < 0.f ? -q8::exp2_int(up) : q8::exp2_int(up);
+    qf = q8::exp2_int(-up) * fabsf(a.scale_log2);
+    unsigned char* dst = sm.q[t] + row * 128;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y[i] = pack_half(__uint_as_float(w[i] << 16) * mul,
+                         __uint_as_float(w[i] & 0xffff0000u) * mul);
+      *reinterpret_cast<uint4*>(dst + (c >> 3) * ATOM + (((c & 7) ^ (row & 7)) << 4)) =
+          make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    ptx::fence_proxy_async();
+    ptx::mbar_arrive(&sm.bars.q_full[t]);
+  }
+
+  __device__ __forceinline__ long out_row(const Unit& u, int h, int r) const {
+    return ((long)u.s.first + r / a.G) * a.Hq + h * a.G + r % a.G;
+  }
+
+  // A chunk's pages as lane j holds them: page j, its scales, log2 of V's.
+  struct Pages {
+    int pid;
+    float ks, vs, lv;
+    __device__ __forceinline__ void scales(const Q8AttendArgs& a, int h) {
+      if (pid >= a.num_pages) pid = -1;
+      ks = vs = 0.f;
+      if (pid >= 0) {
+        ks = a.k_scale[(long)pid * a.Hkv + h];
+        vs = a.v_scale[(long)pid * a.Hkv + h];
+      }
+    }
+  };
+
+  static __device__ __forceinline__ float max32(const uint32_t (&z)[32]) {
+    float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      x0 = fmaxf(x0, __uint_as_float(z[e]));
+      x1 = fmaxf(x1, __uint_as_float(z[e + 1]));
+      x2 = fmaxf(x2, __uint_as_float(z[e + 2]));
+      x3 = fmaxf(x3, __uint_as_float(z[e + 3]));
+    }
+    return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+  }
+
+  // Scores 32 g .. 32 g + 31 that the row does not see become -inf.
+  __device__ __forceinline__ void mask(uint32_t (&z)[32], int g, int key0, bool live) const {
+    const int from = live ? lo - key0 - 32 * g : 32, to = hi - key0 - 32 * g;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < from || e >= to) z[e] = kNegInf;
+  }
+
+  __device__ void run(const Plan& pl, long X0, long X1, int cta, long V, int C) {
+    Bars& B = sm.bars;
+    volatile int* abort = &B.abort;
+    const int lane = threadIdx.x & 31;
+    q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
+    int tiles = 0, units = 0;
+    Walk w;
+    for (w.start(a, pl, X0, X1); !w.done(); w.next(a, pl)) {
+      const Unit& u = w.u;
+      if (t == 1 && u.rows <= 128) continue;
+      load_query(u, w.at.h);
+      float m = -INFINITY, M = -INFINITY, l = 0.f;
+      Pages pg{page_of(a, u, w.key0(0), lane), 0.f, 0.f, 0.f};
+      pg.scales(a, w.at.h);
+#pragma unroll 1
+      for (int i = 0; i < w.n; ++i) {
+        const int key0 = w.key0(i);
+        Pages next{i + 1 < w.n ? page_of(a, u, key0 + CK, lane) : -1, 0.f, 0.f, 0.f};
+        pg.lv = __log2f(pg.vs);
+        const bool gone = lane * a.page < CK && pg.pid < 0;
+        const bool masked =
+            __any_sync(0xffffffffu, gone || key0 < lo || key0 + CK > hi);
+        wait(&B.s_full[t], tiles++, abort, a.err);
+        tc::fence_after_sync();
+        const uint32_t sc = tl + s_col(t);
+        float top = m, ref = M;
+        uint32_t z[32];
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          const int src = 32 * g / a.page;
+          const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
+          const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
+          const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
+          tc::ld32_sync(sc + 32 * g, z);
+          if (masked) mask(z, g, key0, pid >= 0);
+          const float pm = max32(z) * c;
+          top = fmaxf(top, pm);
+          ref = fmaxf(ref, pm + fmaxf(lv, -126.f) - 10.f);
+        }
+        next.scales(a, w.at.h);  // on their way during the exponentials
+        const float base = top == -INFINITY ? 0.f : top;
+        l *= ptx::ex2(m - base);
+        m = top;
+        // M follows when it has fallen behind; O is then rescaled. (S being
+        // full, the products before it, O's included, are complete.)
+        const bool move = ref > M + kLag;
+        const float ao = move && M != -INFINITY ? ptx::ex2(M - ref) : 1.f;
+        if (move) M = ref;
+        if (i > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
+#pragma unroll 1
+          for (int q4 = 0; q4 < 8; ++q4) {
+            uint32_t o[16];
+            const uint32_t oc = tl + o_col(t) + q4 * 16;
+            tc::ld16_sync(oc, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ao);
+            tc::st16(oc, o);
+          }
+        }
+        const float oref = M == -INFINITY ? 0.f : M;
+        // (lanes that hold no page of the chunk have lv = -inf of vs = 0)
+        const float least = warp_min(lane * a.page < CK && pg.pid >= 0 ? pg.lv : INFINITY);
+        const bool apart = __any_sync(
+            0xffffffffu, fabsf(base) > 4194304.f || !(base - oref + least > -60.f));
+        float sum = 0.f;
+        if (!apart) {
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g) {
+            const int src = 32 * g / a.page;
+            const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
+            const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
+            const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
+            tc::ld32_sync(sc + 32 * g, z);
+            if (masked) mask(z, g, key0, pid >= 0);
+            const float off = pid >= 0 ? lv - oref : 0.f;
+            float s0 = 0.f, s1 = 0.f;
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ptx::ex2(fmaf(__uint_as_float(z[2 * e]), c, off));
+              const float p1 = ptx::ex2(fmaf(__uint_as_float(z[2 * e + 1]), c, off));
+              s0 += p0;
+              s1 += p1;
+              p[e] = pack_half(p0, p1);
+            }
+            tc::st16(sc + 16 * g, p);  // over scores that are read already
+            if (pid >= 0) sum = fmaf(s0 + s1, ptx::ex2(oref - base - lv), sum);
+          }
+        } else {
+          // p for itself, from a rounded score (see q8_attend.cu)
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            const int src = 16 * g / a.page;
+            const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
+            const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
+            const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
+            uint32_t y[16], p[8];
+            tc::ld16_sync(sc + 16 * g, y);
+            const float off = pid >= 0 ? base - oref + lv : 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float r[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int key = key0 + 16 * g + e + k;
+                const float d = __fadd_rn(__fmul_rn(__uint_as_float(y[e + k]), c), -base);
+                const bool seen = pid >= 0 && key >= lo && key < hi;
+                sum += seen ? ptx::ex2(d) : 0.f;
+                r[k] = seen ? ptx::ex2(d + off) : 0.f;
+              }
+              p[e / 2] = pack_half(r[0], r[1]);
+            }
+            tc::st8(sc + 8 * g, p);
+          }
+        }
+        l += sum;
+        tc::st_wait();
+        tc::fence_before_sync();
+        ptx::mbar_arrive(&B.p_full[t]);
+        pg = next;
+      }
+
+      // ---- epilogue ----
+      wait(&B.o_full[t], units++, abort, a.err);
+      tc::fence_after_sync();
+      const int r = u.r0 + 128 * t + row;
+      const bool real = r < u.s.n * a.G;
+      const long u0 = w.x - w.at.c;
+      const bool whole = u0 >= X0 && u0 + w.at.nc <= X1;
+      const float base = m == -INFINITY ? 0.f : m, oref = M == -INFINITY ? 0.f : M;
+      // in two factors: 2^(M - m) alone can leave fp32's range
+      const float half = ptx::ex2(0.5f * (oref - base)), f = l == 0.f ? 0.f : half / l;
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+      const int slot = w.seg % kNanSlots;
+      const bool nan = *(volatile int*)&B.nan_flag[slot] != 0;
+      float* part = a.part + (2l * cta + (u0 < X0 ? 0 : 1)) * kPart;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (real ? out_row(u, w.at.h, r) : 0) * D;
+#pragma unroll 1
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint32_t o[32];
+        tc::ld32_sync(tl + o_col(t) + 32 * q4, o);
+        if (!real) continue;
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * half * f;
+        if (nan) {
+          const int tk = r / a.G - u.r0 / a.G;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (sm.nan_rows[slot][32 * q4 + e][tk >> 5] >> (tk & 31) & 1u)
+              y[e] = __uint_as_float(0x7fffffffu);
+        }
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            reinterpret_cast<uint4*>(dst + 32 * q4)[e / 8] =
+                make_uint4(ptx::pack_bf16(y[e], y[e + 1]), ptx::pack_bf16(y[e + 2], y[e + 3]),
+                           ptx::pack_bf16(y[e + 4], y[e + 5]), ptx::pack_bf16(y[e + 6], y[e + 7]));
+        } else {
+          float4* to = reinterpret_cast<float4*>(part + (long)(128 * t + row) * D + 32 * q4);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        }
+      }
+      if (real) {
+        if (whole) {
+          if (a.lse) a.lse[out_row(u, w.at.h, r)] = lse2 * q8::kLn2;
+        } else {
+          part[(long)ROWS * D + 128 * t + row] = lse2;
+        }
+      }
+      if (t == 0 && row == 0 && !whole && u0 < X0 && u0 + w.at.nc <= X1) {
+        mm[cta].unit = (long)w.at.tile * a.Hkv + w.at.h;
+        mm[cta].from = q8::block_of(u0, V, C);
+      }
+      if (nan) {  // (the same for every row of the unit) the marks are used up
+        const int threads = u.rows > 128 ? 256 : 128;
+        ptx::named_bar_sync(1, threads);
+        for (int k = 128 * t + row; k < D * 8; k += threads) (&sm.nan_rows[slot][0][0])[k] = 0;
+        if (t == 0 && row == 0) B.nan_flag[slot] = 0;
+        ptx::named_bar_sync(1, threads);
+      }
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    q8_prefill_tc_kernel(const __grid_constant__ Q8AttendArgs a) {
+  extern __shared__ unsigned char raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  Bars& B = sm.bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(&B.q_full[t], 128);
+      ptx::mbar_init(&B.k_full[t], 128);
+      ptx::mbar_init(&B.k_empty[t], 1);
+      ptx::mbar_init(&B.v_full[t], 128);
+      ptx::mbar_init(&B.v_empty[t], 1);
+      ptx::mbar_init(&B.s_full[t], 1);
+      ptx::mbar_init(&B.p_full[t], 128);
+      ptx::mbar_init(&B.o_full[t], 1);
+    }
+    ptx::mbar_init(&B.fin, 1);
+    B.abort = 0;
+    for (int k = 0; k < kNanSlots; ++k) B.nan_flag[k] = 0;
+    ptx::fence_mbar_init();
+  }
+  for (int k = tid; k < kNanSlots * D * 8; k += kThreads) (&sm.nan_rows[0][0][0])[k] = 0;
+  if (warp == 12) {
+    tc::tmem_alloc(&B.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+
+  Plan pl{a.plan_pre, a.plan_seq, a.plan_base, nullptr, a.plan_base[a.B], 0};
+  const long V = pl.tiles ? pl.pre[pl.tiles] : 0;
+  const int C = (int)max(1l, min((long)gridDim.x, V));
+  const int cta = blockIdx.x;
+  if (tid == 0) reinterpret_cast<q8::MergeMeta*>(a.meta)[cta].unit = -1;
+  __syncthreads();
+  if (cta < C && V > 0) {
+    const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
+    if (warp < 8) {
+      Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane,
+                B.tmem + ((uint32_t)((warp & 3) * 32) << 16), 0.f, 0, 0};
+      s.run(pl, X0, X1, cta, V, C);
+    } else if (warp < 12) {
+      Converter{a, warp - 8, lane}.run(pl, X0, X1, sm);
+    } else if (lane == 0) {
+      issue_mmas(a, pl, X0, X1, sm);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 12) tc::tmem_dealloc(B.tmem, 512);
+}
+
+// Joins the partials of a unit that lies in several blocks: a warp per row of
+// the unit that ends in attention block blockIdx.x (see q8_attend.cuh).
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    q8_prefill_tc_merge_kernel(const __grid_constant__ Q8AttendArgs a) {
+  ptx::grid_dep_wait();
+  const q8::MergeMeta mm = reinterpret_cast<const q8::MergeMeta*>(a.meta)[blockIdx.x];
+  if (mm.unit < 0) return;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int tile = (int)(mm.unit / a.Hkv), h = (int)(mm.unit % a.Hkv);
+  const int b = a.plan_seq[tile];
+  const int r = (tile - a.plan_base[b]) * ROWS + row;
+  int first, n;
+  q8::token_range(a.cu, b, a.N, first, n);
+  if (r >= n * a.G) return;
+  const int np = (int)blockIdx.x - mm.from + 1;
+  auto part = [&](int i) { return a.part + (2l * (mm.from + i) + (i == 0 ? 1 : 0)) * kPart; };
+  float top = -INFINITY;
+  for (int i = lane; i < np; i += 32) top = fmaxf(top, part(i)[(long)ROWS * D + row]);
+  top = warp_max(top);
+  const float base = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < np; ++i) {
+    const float* p = part(i);
+    const float w = ptx::ex2(p[(long)ROWS * D + row] - base);
+    const float4 x = reinterpret_cast<const float4*>(p + (long)row * D)[lane];
+    sum += w;
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const long out = ((long)first + r / a.G) * a.Hq + h * a.G + r % a.G;
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out * D)[lane] =
+      make_uint2(ptx::pack_bf16(acc.x * f, acc.y * f), ptx::pack_bf16(acc.z * f, acc.w * f));
+  if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * q8::kLn2;
+}
+
+}  // namespace
+
+bool q8_prefill_tc_shape(const nsa_params& p) {
+  return p.dtype == NSA_DTYPE_BF16 && p.d == D && p.sel_block >= 32;
+}
+
+size_t q8_prefill_tc_part_bytes() { return (size_t)kPart * 4 * 2 * kQ8MaxBlocks; }
+
+cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, cudaStream_t stream) {
+  constexpr int smem = sizeof(Smem) + 1024;
+  cudaError_t e;
+  if ((e = ensure_dyn_smem((const void*)q8_prefill_tc_kernel, smem)) != cudaSuccess) return e;
+  {
+    TraceScope trace("q8_prefill_tc", stream);
+    if ((e = q8::launch_pdl(q8_prefill_tc_kernel, dim3(a.blocks), dim3(kThreads), smem, stream, a)) !=
+        cudaSuccess)
+      return e;
+  }
+  TraceScope trace("q8_prefill_tc_merge", stream);
+  return q8::launch_pdl(q8_prefill_tc_merge_kernel, dim3(a.blocks, ROWS / kMergeWarps),
+                        dim3(32 * kMergeWarps), 0, stream, a);
+}
+
+}  // namespace nsa
