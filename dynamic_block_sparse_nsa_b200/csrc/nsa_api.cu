@@ -162,12 +162,14 @@ nsa_status check_q8(const nsa_params* p) {
   return NSA_OK;
 }
 
-nsa_status check_q8_cache(const nsa_q8_cache* c) {
+nsa_status check_q8_cache(const nsa_params* p, const nsa_q8_cache* c) {
   if (!c) return fail(NSA_ERR_INVALID_ARGUMENT, "cache is NULL");
   if (!c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->page_table)
     return fail(NSA_ERR_INVALID_ARGUMENT,
                 "k_pages, v_pages, k_scale, v_scale, page_table must be non-NULL");
   if (c->num_pages < 1) return fail(NSA_ERR_INVALID_ARGUMENT, "num_pages must be >= 1");
+  if ((long)c->num_pages * p->Hkv > 0x7fffffffl)
+    return fail(NSA_ERR_UNSUPPORTED, "num_pages * Hkv must be < 2^31");
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages))
     return fail(NSA_ERR_INVALID_ARGUMENT, "k_pages and v_pages must be 16-byte aligned");
   return NSA_OK;
@@ -510,7 +512,7 @@ nsa_status nsa_append_q8(const nsa_params* p, const nsa_q8_cache* cache, const v
   g_detail.clear();
   nsa_status s = check_q8(p);
   if (s != NSA_OK) return s;
-  s = check_q8_cache(cache);
+  s = check_q8_cache(p, cache);
   if (s != NSA_OK) return s;
   if (N < 0 || (!cu_new && N != p->B))
     return fail(NSA_ERR_INVALID_ARGUMENT, "N must be >= 0, and B (%d) without cu_new (got %d)",
@@ -577,7 +579,7 @@ nsa_status nsa_decode_q8(const nsa_params* p, const nsa_q8_cache* cache, const v
   g_detail.clear();
   nsa_status s = check_q8(p);
   if (s != NSA_OK) return s;
-  s = check_q8_cache(cache);
+  s = check_q8_cache(p, cache);
   if (s != NSA_OK) return s;
   if (keys != NSA_KEYS_ALL && keys != NSA_KEYS_WINDOW && keys != NSA_KEYS_BLOCKS)
     return fail(NSA_ERR_INVALID_ARGUMENT, "unknown key set %d", keys);
@@ -607,7 +609,7 @@ nsa_status nsa_prefill_q8(const nsa_params* p, const nsa_q8_cache* cache, const 
   g_detail.clear();
   nsa_status s = check_q8(p);
   if (s != NSA_OK) return s;
-  s = check_q8_cache(cache);
+  s = check_q8_cache(p, cache);
   if (s != NSA_OK) return s;
   if (keys != NSA_KEYS_ALL && keys != NSA_KEYS_WINDOW)
     return fail(NSA_ERR_INVALID_ARGUMENT, "the key set of a prefill is all or window (got %d)", keys);

@@ -85,18 +85,24 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ float warp_min(float x) { return -warp_max(-x); }
-
 // A unit: a tile's rows of one KV head.
 struct Unit {
   Seq s;
-  int b, r0, lo, hi, rows;
+  int b, r0, rows;
+  int lo, hi;            // keys that some row sees
+  int all_lo, all_hi;    // keys that all rows see
+  int tok0, tok1;        // tokens of the rows, of the sequence's new ones
   __device__ __forceinline__ void load(const Q8AttendArgs& a, const Plan& pl, int tile) {
     b = pl.tseq[tile];
     r0 = (tile - pl.tbase[b]) * ROWS;
     s = q8::sequence(a, b);
     rows = min(ROWS, s.n * a.G - r0);
     q8::key_span(a, s, r0, ROWS, lo, hi);
+    tok0 = r0 / a.G;
+    tok1 = (r0 + rows - 1) / a.G;
+    const int at = s.len - s.n;
+    all_hi = hi > 0 ? at + tok0 + 1 : 0;
+    all_lo = a.keys == q8::KEYS_WINDOW ? at + tok1 + 1 - a.window : 0;
   }
 };
 
@@ -130,10 +136,11 @@ struct Walk {
 
 // Lane j's page of the chunk that begins at key0 (j < 128 / page); -1: none,
 // INT_MAX: not a page number.
-__device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int key0, int lane) {
-  const int first = key0 + lane * a.page;
-  if (lane * a.page >= CK || first >= u.hi) return -1;
-  const int pid = a.table[(long)u.b * a.max_pages + first / a.page];
+__device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int key0, int lane,
+                                       int shift) {
+  const int first = key0 + (lane << shift);
+  if (lane >= CK >> shift || first >= u.hi) return -1;
+  const int pid = a.table[(long)u.b * a.max_pages + (first >> shift)];
   return pid < 0 ? INT_MAX : pid;
 }
 
@@ -142,18 +149,32 @@ __device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int
 struct Converter {
   const Q8AttendArgs& a;
   int warp, lane;  // of the four
+  int shift;       // log2 of the page
   __device__ __forceinline__ int row(int k) const { return 16 * k + 4 * warp + (lane >> 3); }
 
-  __device__ __forceinline__ void load(uint4 (&x)[8], const uint8_t* pages, const Unit& u, int h,
-                                       int key0, int pid) const {
+  // The lane's pieces of the chunk: 16 bytes of row(k). Lane j holds the place
+  // (page * Hkv + head) of page j of the chunk.
+  __device__ __forceinline__ void load(uint4 (&x)[8], const uint8_t* pages, const Unit& u,
+                                       int key0, int place) const {
+    const uint8_t* base = pages + ((4 * warp + (lane >> 3)) * D + (lane & 7) * 16);
+    const int mask = (1 << shift) - 1;
+    if (key0 >= u.lo && key0 + CK <= u.hi &&
+        !__any_sync(0xffffffffu, lane < CK >> shift && place < 0)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = row(k), p = __shfl_sync(0xffffffffu, pid, 16 * k / a.page);
-      const int pos = key0 + r;
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (p >= 0 && pos >= u.lo && pos < u.hi)
-        x[k] = __ldg(reinterpret_cast<const uint4*>(
-            pages + (((long)p * a.Hkv + h) * a.page + (r & (a.page - 1))) * D + (lane & 7) * 16));
+      for (int k = 0; k < 8; ++k) {
+        const int p = __shfl_sync(0xffffffffu, place, (16 * k) >> shift);
+        x[k] = __ldg(reinterpret_cast<const uint4*>(base + ((long)p << (shift + 7)) +
+                                                    ((16 * k) & mask) * D));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int p = __shfl_sync(0xffffffffu, place, (16 * k) >> shift), pos = key0 + row(k);
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (p >= 0 && pos >= u.lo && pos < u.hi)
+          x[k] = __ldg(reinterpret_cast<const uint4*>(base + ((long)p << (shift + 7)) +
+                                                      ((16 * k) & mask) * D));
+      }
     }
   }
 
@@ -184,7 +205,8 @@ struct Converter {
 
   // NaN values of keys that only some of the tile's tokens see: marked for
   // those, and replaced by zeros (0 * NaN would reach the others).
-  __device__ void mark_nan(uint4 (&x)[8], const Unit& u, int key0, uint32_t (*marks)[8],
+  // at0: position of the tile's first token, last: index of its last.
+  __device__ void mark_nan(uint4 (&x)[8], int at0, int last, int key0, uint32_t (*marks)[8],
                            int* flag) const {
     bool found = false;
 #pragma unroll
@@ -194,15 +216,12 @@ struct Converter {
       for (int i = 0; i < 4; ++i) found |= __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
     }
     if (!found) return;
-    const int tok0 = u.r0 / a.G, tok1 = (u.r0 + u.rows - 1) / a.G;
-    const int at0 = u.s.len - u.s.n + tok0;  // position of the tile's first token
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
       const int key = key0 + row(k);
       const int from = max(0, key - at0);
-      const int to = a.keys == q8::KEYS_WINDOW ? min(tok1 - tok0, key - at0 + a.window - 1)
-                                               : tok1 - tok0;
+      const int to = a.keys == q8::KEYS_WINDOW ? min(last, key - at0 + a.window - 1) : last;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t bad = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -225,39 +244,40 @@ struct Converter {
     Walk w;
     w.start(a, pl, X0, X1);
     int i = 0;  // chunk of the segment
-    int key0 = w.key0(0), h = w.at.h, slot = 0;
-    Unit u = w.u;
-    int pid = check(page_of(a, u, key0, lane));
+    int key0 = w.key0(0), slot = 0;
+    const Unit& u = w.u;  // of the chunk whose pages were looked up last
+    int place = place_of(page_of(a, u, key0, lane, shift), w.at.h);
     uint4 kx[8], vx[8];
-    load(kx, a.k_pages, u, h, key0, pid);
+    load(kx, a.k_pages, u, key0, place);
     const int len = (int)(X1 - X0);
+#pragma unroll 1
     for (int j = 0; j < len; ++j) {
       const int buf = j & 1;
-      load(vx, a.v_pages, u, h, key0, pid);
-      // the next chunk's pages
-      const Unit un = u;
+      load(vx, a.v_pages, u, key0, place);
+      const bool edge = key0 + CK > u.all_hi || key0 < u.all_lo;
       const int kn = key0, sn = slot;
+      // the next chunk's pages
       const bool more = j + 1 < len;
+      int pid = -1;
+      const int at0 = u.s.len - u.s.n + u.tok0, last = u.tok1 - u.tok0;
       if (more) {
         if (++i == w.n) {
           w.next(a, pl);
           i = 0;
-          u = w.u;
-          h = w.at.h;
           slot = w.seg % kNanSlots;
         }
         key0 = w.key0(i);
-        pid = page_of(a, u, key0, lane);
+        pid = page_of(a, u, key0, lane, shift);
       }
       if (j >= 2) wait(&B.k_empty[buf], (j >> 1) - 1, abort, a.err);
       store(kx, sm.k[buf]);
       ptx::fence_proxy_async();
       ptx::mbar_arrive(&B.k_full[buf]);
       if (more) {
-        pid = check(pid);
-        load(kx, a.k_pages, u, h, key0, pid);
+        place = place_of(pid, w.at.h);
+        load(kx, a.k_pages, u, key0, place);
       }
-      if (edge(un, kn)) mark_nan(vx, un, kn, sm.nan_rows[sn], &B.nan_flag[sn]);
+      if (edge) mark_nan(vx, at0, last, kn, sm.nan_rows[sn], &B.nan_flag[sn]);
       if (j >= 2) wait(&B.v_empty[buf], (j >> 1) - 1, abort, a.err);
       store(vx, sm.v[buf]);
       ptx::fence_proxy_async();
@@ -265,20 +285,12 @@ struct Converter {
     }
   }
 
-  // Whether some token of the tile does not see all of the chunk.
-  __device__ __forceinline__ bool edge(const Unit& u, int key0) const {
-    const int tok0 = u.r0 / a.G, tok1 = (u.r0 + u.rows - 1) / a.G;
-    const int at0 = u.s.len - u.s.n;
-    return key0 + CK > at0 + tok0 + 1 ||
-           (a.keys == q8::KEYS_WINDOW && key0 < at0 + tok1 + 1 - a.window);
-  }
-
-  __device__ __forceinline__ int check(int pid) const {
+  __device__ __forceinline__ int place_of(int pid, int h) const {
     if (pid >= a.num_pages) {
       atomicOr(a.err, kErrPage);
       return -1;
     }
-    return pid;
+    return pid < 0 ? -1 : pid * a.Hkv + h;
   }
 };
 
@@ -344,6 +356,7 @@ struct Softmax {
   Smem& sm;
   int t, row;      // half, row of it
   uint32_t tl;     // the warp's lanes of tensor memory
+  int shift;       // log2 of the page
   float qf;        // row factor of the scores
   int lo, hi;      // keys the row sees
 
@@ -443,14 +456,14 @@ struct Softmax {
       if (t == 1 && u.rows <= 128) continue;
       load_query(u, w.at.h);
       float m = -INFINITY, M = -INFINITY, l = 0.f;
-      Pages pg{page_of(a, u, w.key0(0), lane), 0.f, 0.f, 0.f};
+      Pages pg{page_of(a, u, w.key0(0), lane, shift), 0.f, 0.f, 0.f};
       pg.scales(a, w.at.h);
 #pragma unroll 1
       for (int i = 0; i < w.n; ++i) {
         const int key0 = w.key0(i);
-        Pages next{i + 1 < w.n ? page_of(a, u, key0 + CK, lane) : -1, 0.f, 0.f, 0.f};
+        Pages next{i + 1 < w.n ? page_of(a, u, key0 + CK, lane, shift) : -1, 0.f, 0.f, 0.f};
         pg.lv = __log2f(pg.vs);
-        const bool gone = lane * a.page < CK && pg.pid < 0;
+        const bool gone = lane < CK >> shift && pg.pid < 0;
         const bool masked =
             __any_sync(0xffffffffu, gone || key0 < lo || key0 + CK > hi);
         wait(&B.s_full[t], tiles++, abort, a.err);
@@ -460,7 +473,7 @@ struct Softmax {
         uint32_t z[32];
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
-          const int src = 32 * g / a.page;
+          const int src = (32 * g) >> shift;
           const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
           const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
           const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
@@ -491,15 +504,15 @@ struct Softmax {
           }
         }
         const float oref = M == -INFINITY ? 0.f : M;
-        // (lanes that hold no page of the chunk have lv = -inf of vs = 0)
-        const float least = warp_min(lane * a.page < CK && pg.pid >= 0 ? pg.lv : INFINITY);
+        const int least = __reduce_min_sync(
+            0xffffffffu, lane < CK >> shift && pg.pid >= 0 ? __float2int_rd(pg.lv) : INT_MAX);
         const bool apart = __any_sync(
-            0xffffffffu, fabsf(base) > 4194304.f || !(base - oref + least > -60.f));
+            0xffffffffu, fabsf(base) > 4194304.f || !(base - oref + (float)least > -60.f));
         float sum = 0.f;
         if (!apart) {
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {
-            const int src = 32 * g / a.page;
+            const int src = (32 * g) >> shift;
             const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
             const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
             const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
@@ -523,7 +536,7 @@ struct Softmax {
           // p for itself, from a rounded score (see q8_attend.cu)
 #pragma unroll 1
           for (int g = 0; g < 8; ++g) {
-            const int src = 16 * g / a.page;
+            const int src = (16 * g) >> shift;
             const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
             const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
             const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
@@ -577,7 +590,7 @@ struct Softmax {
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * half * f;
         if (nan) {
-          const int tk = r / a.G - u.r0 / a.G;
+          const int tk = r / a.G - u.tok0;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (sm.nan_rows[slot][32 * q4 + e][tk >> 5] >> (tk & 31) & 1u)
@@ -659,12 +672,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (cta < C && V > 0) {
     const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
+    const int shift = __ffs(a.page) - 1;
     if (warp < 8) {
       Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane,
-                B.tmem + ((uint32_t)((warp & 3) * 32) << 16), 0.f, 0, 0};
+                B.tmem + ((uint32_t)((warp & 3) * 32) << 16), shift, 0.f, 0, 0};
       s.run(pl, X0, X1, cta, V, C);
     } else if (warp < 12) {
-      Converter{a, warp - 8, lane}.run(pl, X0, X1, sm);
+      Converter{a, warp - 8, lane, shift}.run(pl, X0, X1, sm);
     } else if (lane == 0) {
       issue_mmas(a, pl, X0, X1, sm);
     }
