@@ -11,11 +11,12 @@
 //   warps 0-3, 4-7   softmax of a half, a thread per row: S from tensor memory,
 //                    P back over it, O rescaled when its reference moves by
 //                    more than 2^5, the epilogue;
-//   warps 8-11       codes from global memory to fp16 K and V tiles in shared
-//                    memory (128-byte swizzle), two buffers each, the next
-//                    tile's codes in flight in registers meanwhile;
+//   warps 8-11       codes to fp16 K and V tiles in shared memory (128-byte
+//                    swizzle), a ring of three;
 //   warp 12          issues the MMAs: while one half's softmax runs, the other
-//                    half's products do.
+//                    half's products do;
+//   warp 13          copies the pages' codes to shared memory (a head's page is
+//                    contiguous: one bulk copy each), three tiles ahead.
 // The bound is the softmax: an exponential for every score (16 a clock and SM)
 // takes as long as the two products of it.
 #include <cuda.h>
@@ -37,10 +38,12 @@ constexpr int ROWS = kQ8TcRows;
 constexpr int CK = kQ8TcKeys;
 constexpr uint32_t ATOM = 16384;   // 128 rows x 64 halves
 constexpr uint32_t TILE = 32768;   // 128 rows x 128 halves
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kNegInf = 0xff800000u;
 constexpr float kLag = 5.f;        // how far M may fall behind before O is rescaled
+constexpr int kRing = 3;           // fp16 tiles: K of chunk 0, V of it, K of chunk 1, ...
+constexpr int kRaw = 3;            // tiles of codes under way
 constexpr int kNanSlots = 4;       // units whose NaN marks are under way
 constexpr long kPart = (long)ROWS * D + ROWS;  // floats of a partial: o, lse2
 
@@ -49,17 +52,19 @@ __device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
 __device__ __forceinline__ uint32_t o_col(int t) { return 256u + 128u * t; }
 
 struct Bars {
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t full[kRing], empty[kRing], raw_full[kRaw], raw_empty[kRaw];
   uint64_t fin;
   int abort;
   uint32_t tmem;
   int nan_flag[kNanSlots];
+  uint32_t live[kRaw];  // pages of the tile that were copied, a bit each
 };
 
 struct Smem {
   unsigned char q[2][TILE];
-  unsigned char k[2][TILE];
-  unsigned char v[2][TILE];
+  unsigned char kv[kRing][TILE];
+  unsigned char raw[kRaw][CK * D];
   Bars bars;
   uint32_t nan_rows[kNanSlots][D][8];  // per component: the tile's tokens that see a NaN value
 };
@@ -73,12 +78,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-__device__ __forceinline__ uint64_t kmaj(uint32_t base, int ks) {
-  return tc::sdesc(base + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024, tc::kSw128);
+// Descriptor of the 16-component step ks of an operand whose first step's
+// descriptor is d: K-major (32 bytes a step, four to a 64-component atom), or
+// MN-major (16 rows of 128 bytes a step). The address field counts 16 bytes.
+__device__ __forceinline__ uint64_t k_step(uint64_t d, int ks) {
+  return d + (((ks >> 2) * ATOM + (ks & 3) * 32) >> 4);
 }
-__device__ __forceinline__ uint64_t mnmaj(uint32_t base, int ks) {
-  return tc::sdesc(base + ks * 2048, ATOM, 1024, tc::kSw128);
-}
+__device__ __forceinline__ uint64_t mn_step(uint64_t d, int ks) { return d + ((ks * 2048) >> 4); }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -144,6 +150,55 @@ __device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int
   return pid < 0 ? INT_MAX : pid;
 }
 
+// ---- pages to shared memory (one warp) -------------------------------------------
+
+__device__ void copy_pages(const Q8AttendArgs& a, const Plan& pl, long X0, long X1, Smem& sm,
+                           int shift, int lane) {
+  Bars& B = sm.bars;
+  volatile int* abort = &B.abort;
+  const int chunks = (int)(X1 - X0);
+  const uint32_t bytes = (uint32_t)D << shift;
+  Walk w;
+  w.start(a, pl, X0, X1);
+  int i = 0;
+  int pid = page_of(a, w.u, w.key0(0), lane, shift);  // lane j: page j of the chunk
+  bool ok = true;
+  int n = 0;
+  for (int j = 0; ok && j < chunks; ++j) {
+    if (pid >= a.num_pages) {
+      atomicOr(a.err, kErrPage);
+      pid = -1;
+    }
+    const bool mine = pid >= 0;
+    const uint32_t live = __ballot_sync(0xffffffffu, mine);
+    const long from = ((long)pid * a.Hkv + w.at.h) << (shift + 7);
+    if (++i == w.n) {
+      w.next(a, pl);
+      i = 0;
+    }
+    pid = w.done() ? -1 : page_of(a, w.u, w.key0(i), lane, shift);
+    for (int v = 0; ok && v < 2; ++v, ++n) {
+      const int r = n % kRaw;
+      if (n >= kRaw) ok = wait(&B.raw_empty[r], n / kRaw - 1, abort, a.err);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        B.live[r] = live;
+        ptx::mbar_arrive_expect_tx(&B.raw_full[r], __popc(live) * bytes);
+      }
+      __syncwarp();
+      if (mine)
+        ptx::bulk_load(sm.raw[r] + lane * bytes, (v ? a.v_pages : a.k_pages) + from, bytes,
+                       &B.raw_full[r]);
+    }
+  }
+  // every copy has landed before the block ends
+  for (int k = n > kRaw ? n - kRaw : 0; k < n; ++k)
+    if (!ptx::mbar_wait(&B.raw_full[k % kRaw], (k / kRaw) & 1, kWaitNs)) atomicOr(a.err, kErrTimeout);
+}
+
 // ---- codes to fp16 tiles ------------------------------------------------------
 
 struct Converter {
@@ -151,32 +206,6 @@ struct Converter {
   int warp, lane;  // of the four
   int shift;       // log2 of the page
   __device__ __forceinline__ int row(int k) const { return 16 * k + 4 * warp + (lane >> 3); }
-
-  // The lane's pieces of the chunk: 16 bytes of row(k). Lane j holds the place
-  // (page * Hkv + head) of page j of the chunk.
-  __device__ __forceinline__ void load(uint4 (&x)[8], const uint8_t* pages, const Unit& u,
-                                       int key0, int place) const {
-    const uint8_t* base = pages + ((4 * warp + (lane >> 3)) * D + (lane & 7) * 16);
-    const int mask = (1 << shift) - 1;
-    if (key0 >= u.lo && key0 + CK <= u.hi &&
-        !__any_sync(0xffffffffu, lane < CK >> shift && place < 0)) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int p = __shfl_sync(0xffffffffu, place, (16 * k) >> shift);
-        x[k] = __ldg(reinterpret_cast<const uint4*>(base + ((long)p << (shift + 7)) +
-                                                    ((16 * k) & mask) * D));
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int p = __shfl_sync(0xffffffffu, place, (16 * k) >> shift), pos = key0 + row(k);
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (p >= 0 && pos >= u.lo && pos < u.hi)
-          x[k] = __ldg(reinterpret_cast<const uint4*>(base + ((long)p << (shift + 7)) +
-                                                      ((16 * k) & mask) * D));
-      }
-    }
-  }
 
   // Row r's 16 components as two 16-byte pieces of the swizzled tile; lanes of
   // the second half store theirs in the other order, so that the eight lanes
@@ -241,56 +270,42 @@ struct Converter {
   __device__ void run(const Plan& pl, long X0, long X1, Smem& sm) const {
     Bars& B = sm.bars;
     volatile int* abort = &B.abort;
+    const int tiles = 2 * (int)(X1 - X0);
     Walk w;
     w.start(a, pl, X0, X1);
-    int i = 0;  // chunk of the segment
-    int key0 = w.key0(0), slot = 0;
-    const Unit& u = w.u;  // of the chunk whose pages were looked up last
-    int place = place_of(page_of(a, u, key0, lane, shift), w.at.h);
-    uint4 kx[8], vx[8];
-    load(kx, a.k_pages, u, key0, place);
-    const int len = (int)(X1 - X0);
+    int i = 0;
 #pragma unroll 1
-    for (int j = 0; j < len; ++j) {
-      const int buf = j & 1;
-      load(vx, a.v_pages, u, key0, place);
-      const bool edge = key0 + CK > u.all_hi || key0 < u.all_lo;
-      const int kn = key0, sn = slot;
-      // the next chunk's pages
-      const bool more = j + 1 < len;
-      int pid = -1;
-      const int at0 = u.s.len - u.s.n + u.tok0, last = u.tok1 - u.tok0;
-      if (more) {
-        if (++i == w.n) {
-          w.next(a, pl);
-          i = 0;
-          slot = w.seg % kNanSlots;
+    for (int n = 0; n < tiles; ++n) {
+      const int r = n % kRaw, buf = n % kRing;
+      wait(&B.raw_full[r], n / kRaw, abort, a.err);
+      const uint32_t live = B.live[r];
+      uint4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = *reinterpret_cast<const uint4*>(sm.raw[r] + row(k) * D + (lane & 7) * 16);
+      ptx::mbar_arrive(&B.raw_empty[r]);
+      const int key0 = w.key0(i);
+      if (key0 + CK > w.u.all_hi || key0 < w.u.all_lo || live != (1u << (CK >> shift)) - 1) {
+        // rows that no token sees hold anything: zeros
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int pos = key0 + row(k);
+          if (pos < w.u.lo || pos >= w.u.hi || !(live >> (row(k) >> shift) & 1u))
+            x[k] = make_uint4(0, 0, 0, 0);
         }
-        key0 = w.key0(i);
-        pid = page_of(a, u, key0, lane, shift);
+        if (n & 1)
+          mark_nan(x, w.u.s.len - w.u.s.n + w.u.tok0, w.u.tok1 - w.u.tok0, key0,
+                   sm.nan_rows[w.seg % kNanSlots], &B.nan_flag[w.seg % kNanSlots]);
       }
-      if (j >= 2) wait(&B.k_empty[buf], (j >> 1) - 1, abort, a.err);
-      store(kx, sm.k[buf]);
-      ptx::fence_proxy_async();
-      ptx::mbar_arrive(&B.k_full[buf]);
-      if (more) {
-        place = place_of(pid, w.at.h);
-        load(kx, a.k_pages, u, key0, place);
+      if ((n & 1) && ++i == w.n) {
+        w.next(a, pl);
+        i = 0;
       }
-      if (edge) mark_nan(vx, at0, last, kn, sm.nan_rows[sn], &B.nan_flag[sn]);
-      if (j >= 2) wait(&B.v_empty[buf], (j >> 1) - 1, abort, a.err);
-      store(vx, sm.v[buf]);
+      if (n >= kRing) wait(&B.empty[buf], n / kRing - 1, abort, a.err);
+      store(x, sm.kv[buf]);
       ptx::fence_proxy_async();
-      ptx::mbar_arrive(&B.v_full[buf]);
+      ptx::mbar_arrive(&B.full[buf]);
     }
-  }
-
-  __device__ __forceinline__ int place_of(int pid, int h) const {
-    if (pid >= a.num_pages) {
-      atomicOr(a.err, kErrPage);
-      return -1;
-    }
-    return pid < 0 ? -1 : pid * a.Hkv + h;
   }
 };
 
@@ -302,45 +317,50 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
   const uint32_t tmem = B.tmem;
   constexpr uint32_t iqk = tc::idesc_f16(128, 128, false, false);
   constexpr uint32_t ipv = tc::idesc_f16(128, 128, false, true);
-  const uint32_t q0 = ptx::smem_u32(sm.q), k0 = ptx::smem_u32(sm.k), v0 = ptx::smem_u32(sm.v);
+  const uint64_t dq = tc::sdesc(ptx::smem_u32(sm.q), 16, 1024, tc::kSw128);
+  const uint64_t dk = tc::sdesc(ptx::smem_u32(sm.kv), 16, 1024, tc::kSw128);
+  const uint64_t dv = tc::sdesc(ptx::smem_u32(sm.kv), ATOM, 1024, tc::kSw128);
   int segs[2] = {0, 0}, tiles[2] = {0, 0};  // per half: units begun, P tiles taken
   Walk w;
   bool ok = true;
-  int j = 0;  // the block's chunk
+  int n = 0;  // the block's K tile (its V tile is n + 1)
   for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
     const int halves = w.u.rows > 128 ? 2 : 1;
-    auto qk = [&](int t, int jj) {
-      const uint32_t kb = k0 + (jj & 1) * TILE;
+    auto ready = [&](int k) {
+      const bool r = wait(&B.full[k % kRing], k / kRing, abort, a.err);
+      tc::fence_after_sync();
+      return r;
+    };
+    auto qk = [&](int t, int k) {
+      const uint64_t qt = dq + ((t * TILE) >> 4), kt = dk + (((k % kRing) * TILE) >> 4);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        tc::mma_ss(tmem + s_col(t), kmaj(q0 + t * TILE, ks), kmaj(kb, ks), iqk, ks > 0);
-      if (t == halves - 1) tc::commit(&B.k_empty[jj & 1]);
+        tc::mma_ss(tmem + s_col(t), k_step(qt, ks), k_step(kt, ks), iqk, ks > 0);
+      if (t == halves - 1) tc::commit(&B.empty[k % kRing]);
       tc::commit(&B.s_full[t]);
     };
     for (int t = 0; t < halves; ++t) ok = ok && wait(&B.q_full[t], segs[t]++, abort, a.err);
-    ok = ok && wait(&B.k_full[j & 1], j >> 1, abort, a.err);
+    ok = ok && ready(n);
     if (!ok) break;
-    tc::fence_after_sync();
-    for (int t = 0; t < halves; ++t) qk(t, j);
-    for (int i = 0; ok && i < w.n; ++i, ++j) {
+    for (int t = 0; t < halves; ++t) qk(t, n);
+    for (int i = 0; ok && i < w.n; ++i, n += 2) {
       const bool more = i + 1 < w.n;
-      ok = wait(&B.v_full[j & 1], j >> 1, abort, a.err);
+      ok = ready(n + 1);
       for (int t = 0; ok && t < halves; ++t) {
         ok = wait(&B.p_full[t], tiles[t]++, abort, a.err);
         if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t vb = v0 + (j & 1) * TILE;
+        const uint64_t vt = dv + ((((n + 1) % kRing) * TILE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mnmaj(vb, ks), ipv, (i > 0 || ks > 0));
-        if (t == halves - 1) tc::commit(&B.v_empty[j & 1]);
-        if (!more) tc::commit(&B.o_full[t]);
-        if (more) {
-          if (t == 0) {
-            ok = wait(&B.k_full[(j + 1) & 1], (j + 1) >> 1, abort, a.err);
-            tc::fence_after_sync();
-          }
-          if (ok) qk(t, j + 1);
+          tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mn_step(vt, ks), ipv,
+                     (i > 0 || ks > 0));
+        if (t == halves - 1) tc::commit(&B.empty[(n + 1) % kRing]);
+        if (!more) {
+          tc::commit(&B.o_full[t]);
+        } else {
+          if (t == 0) ok = ready(n + 2);
+          if (ok) qk(t, n + 2);
         }
       }
     }
@@ -470,18 +490,28 @@ struct Softmax {
         tc::fence_after_sync();
         const uint32_t sc = tl + s_col(t);
         float top = m, ref = M;
-        uint32_t z[32];
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
+        uint32_t z0[32], z1[32];
+        // (the next 32 scores are on their way from tensor memory meanwhile)
+        auto largest = [&](uint32_t (&z)[32], int g) {
           const int src = (32 * g) >> shift;
           const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
           const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
           const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
-          tc::ld32_sync(sc + 32 * g, z);
           if (masked) mask(z, g, key0, pid >= 0);
           const float pm = max32(z) * c;
           top = fmaxf(top, pm);
           ref = fmaxf(ref, pm + fmaxf(lv, -126.f) - 10.f);
+        };
+        tc::ld32_nowait(sc, z0);
+        tc::ld_wait32(z0);
+#pragma unroll 1
+        for (int g = 0; g < 4; g += 2) {
+          tc::ld32_nowait(sc + 32 * g + 32, z1);
+          largest(z0, g);
+          tc::ld_wait32(z1);
+          tc::ld32_nowait(sc + (32 * g + 64) % 128, z0);  // at the end: for the next pass
+          largest(z1, g + 1);
+          tc::ld_wait32(z0);
         }
         next.scales(a, w.at.h);  // on their way during the exponentials
         const float base = top == -INFINITY ? 0.f : top;
@@ -510,13 +540,11 @@ struct Softmax {
             0xffffffffu, fabsf(base) > 4194304.f || !(base - oref + (float)least > -60.f));
         float sum = 0.f;
         if (!apart) {
-#pragma unroll 1
-          for (int g = 0; g < 4; ++g) {
+          auto weights = [&](uint32_t (&z)[32], int g) {
             const int src = (32 * g) >> shift;
             const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
             const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
             const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
-            tc::ld32_sync(sc + 32 * g, z);
             if (masked) mask(z, g, key0, pid >= 0);
             const float off = pid >= 0 ? lv - oref : 0.f;
             float s0 = 0.f, s1 = 0.f;
@@ -531,6 +559,15 @@ struct Softmax {
             }
             tc::st16(sc + 16 * g, p);  // over scores that are read already
             if (pid >= 0) sum = fmaf(s0 + s1, ptx::ex2(oref - base - lv), sum);
+          };
+#pragma unroll 1
+          for (int g = 0; g < 4; g += 2) {
+            tc::ld32_nowait(sc + 32 * g + 32, z1);
+            weights(z0, g);
+            tc::ld_wait32(z1);
+            if (g == 0) tc::ld32_nowait(sc + 64, z0);
+            weights(z1, g + 1);
+            if (g == 0) tc::ld_wait32(z0);
           }
         } else {
           // p for itself, from a rounded score (see q8_attend.cu)
@@ -640,13 +677,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&B.q_full[t], 128);
-      ptx::mbar_init(&B.k_full[t], 128);
-      ptx::mbar_init(&B.k_empty[t], 1);
-      ptx::mbar_init(&B.v_full[t], 128);
-      ptx::mbar_init(&B.v_empty[t], 1);
       ptx::mbar_init(&B.s_full[t], 1);
       ptx::mbar_init(&B.p_full[t], 128);
       ptx::mbar_init(&B.o_full[t], 1);
+    }
+    for (int k = 0; k < kRing; ++k) {
+      ptx::mbar_init(&B.full[k], 128);
+      ptx::mbar_init(&B.empty[k], 1);
+    }
+    for (int k = 0; k < kRaw; ++k) {
+      ptx::mbar_init(&B.raw_full[k], 1);
+      ptx::mbar_init(&B.raw_empty[k], 128);
     }
     ptx::mbar_init(&B.fin, 1);
     B.abort = 0;
@@ -679,6 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.run(pl, X0, X1, cta, V, C);
     } else if (warp < 12) {
       Converter{a, warp - 8, lane, shift}.run(pl, X0, X1, sm);
+    } else if (warp == 13) {
+      copy_pages(a, pl, X0, X1, sm, shift, lane);
     } else if (lane == 0) {
       issue_mmas(a, pl, X0, X1, sm);
     }
