@@ -38,9 +38,8 @@ constexpr int ROWS = kQ8TcRows;
 constexpr int CK = kQ8TcKeys;
 constexpr uint32_t ATOM = 16384;   // 128 rows x 64 halves
 constexpr uint32_t TILE = 32768;   // 128 rows x 128 halves
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = 16 * 32;  // (warps 14 and 15 only give registers away)
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kNegInf = 0xff800000u;
 constexpr float kLag = 5.f;        // how far M may fall behind before O is rescaled
 constexpr int kRing = 3;           // fp16 tiles: K of chunk 0, V of it, K of chunk 1, ...
 constexpr int kRaw = 3;            // tiles of codes under way
@@ -85,6 +84,26 @@ __device__ __forceinline__ uint64_t k_step(uint64_t d, int ks) {
   return d + (((ks >> 2) * ATOM + (ks & 3) * 32) >> 4);
 }
 __device__ __forceinline__ uint64_t mn_step(uint64_t d, int ks) { return d + ((ks * 2048) >> 4); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -385,8 +404,9 @@ struct Softmax {
     const int r = u.r0 + 128 * t + row;
     const bool real = r < u.s.n * a.G;
     const int pos = u.s.len - u.s.n + r / a.G;
-    hi = real && u.hi > 0 ? pos + 1 : 0;
-    lo = a.keys == q8::KEYS_WINDOW ? max(0, pos + 1 - a.window) : 0;
+    // (rows behind the last see everything: their warps need no masks)
+    hi = !real ? INT_MAX / 2 : u.hi > 0 ? pos + 1 : 0;
+    lo = real && a.keys == q8::KEYS_WINDOW ? max(0, pos + 1 - a.window) : 0;
     uint4 x[16];
     const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const __nv_bfloat16*>(a.q) + (real ? out_row(u, h, r) : 0) * D);
@@ -444,6 +464,36 @@ struct Softmax {
     }
   };
 
+  // The running maximum and reference after 32 scores.
+  static __device__ __forceinline__ void largest(const uint32_t (&z)[32], float c, float lv,
+                                                 float& top, float& ref) {
+    const float pm = max32(z) * c;
+    top = fmaxf(top, pm);
+    ref = fmaxf(ref, pm + fmaxf(lv, -126.f) - 10.f);
+  }
+
+  // p * vscale in units of 2^M of 32 scores, as halves to tensor memory (over
+  // scores that are read already); sum += p.
+  static __device__ __forceinline__ void weights(const uint32_t (&z)[32], uint32_t to, float c,
+                                                 float lv, float oref, float base, float& sum) {
+    const uint64_t cc = pack2(c, c), off = pack2(lv - oref, lv - oref);
+    uint64_t s = pack2(0.f, 0.f);
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float p0, p1;
+      unpack2(fma2(pack2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), cc, off), p0, p1);
+      p0 = ptx::ex2(p0);
+      p1 = ptx::ex2(p1);
+      s = add2(s, pack2(p0, p1));
+      p[e] = pack_half(p0, p1);
+    }
+    tc::st16(to, p);
+    float s0, s1;
+    unpack2(s, s0, s1);
+    sum = fmaf(s0 + s1, ptx::ex2(oref - base - lv), sum);
+  }
+
   static __device__ __forceinline__ float max32(const uint32_t (&z)[32]) {
     float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
 #pragma unroll
@@ -456,12 +506,14 @@ struct Softmax {
     return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
   }
 
-  // Scores 32 g .. 32 g + 31 that the row does not see become -inf.
-  __device__ __forceinline__ void mask(uint32_t (&z)[32], int g, int key0, bool live) const {
-    const int from = live ? lo - key0 - 32 * g : 32, to = hi - key0 - 32 * g;
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e < from || e >= to) z[e] = kNegInf;
+  // The unit's NaN marks, if any, are used up (every row's thread sees the same flag).
+  __device__ void use_marks(const Unit& u, int slot) const {
+    if (!*(volatile int*)&sm.bars.nan_flag[slot]) return;
+    const int threads = u.rows > 128 ? 256 : 128;
+    ptx::named_bar_sync(1, threads);
+    for (int k = 128 * t + row; k < D * 8; k += threads) (&sm.nan_rows[slot][0][0])[k] = 0;
+    if (t == 0 && row == 0) sm.bars.nan_flag[slot] = 0;
+    ptx::named_bar_sync(1, threads);
   }
 
   __device__ void run(const Plan& pl, long X0, long X1, int cta, long V, int C) {
@@ -475,6 +527,16 @@ struct Softmax {
       const Unit& u = w.u;
       if (t == 1 && u.rows <= 128) continue;
       load_query(u, w.at.h);
+      if (u.rows <= 128 * t + (row & ~31)) {  // no row of the warp is real
+        for (int i = 0; i < w.n; ++i) {
+          wait(&B.s_full[t], tiles++, abort, a.err);
+          ptx::mbar_arrive(&B.p_full[t]);
+        }
+        wait(&B.o_full[t], units++, abort, a.err);
+        // (it has read the marks' flag like the others)
+        use_marks(u, w.seg % kNanSlots);
+        continue;
+      }
       float m = -INFINITY, M = -INFINITY, l = 0.f;
       Pages pg{page_of(a, u, w.key0(0), lane, shift), 0.f, 0.f, 0.f};
       pg.scales(a, w.at.h);
@@ -483,35 +545,53 @@ struct Softmax {
         const int key0 = w.key0(i);
         Pages next{i + 1 < w.n ? page_of(a, u, key0 + CK, lane, shift) : -1, 0.f, 0.f, 0.f};
         pg.lv = __log2f(pg.vs);
-        const bool gone = lane < CK >> shift && pg.pid < 0;
-        const bool masked =
-            __any_sync(0xffffffffu, gone || key0 < lo || key0 + CK > hi);
+        const bool mine = lane < CK >> shift;
+        const bool masked = __any_sync(
+            0xffffffffu, (mine && pg.pid < 0) || key0 < lo || key0 + CK > hi);
+        const int least = __reduce_min_sync(
+            0xffffffffu, mine && pg.pid >= 0 ? __float2int_rd(pg.lv) : INT_MAX);
+        float c[4], lv[4];  // of 32 scores each
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          c[g] = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, (32 * g) >> shift), 1.17549435e-38f);
+          lv[g] = __shfl_sync(0xffffffffu, pg.lv, (32 * g) >> shift);
+        }
         wait(&B.s_full[t], tiles++, abort, a.err);
         tc::fence_after_sync();
         const uint32_t sc = tl + s_col(t);
         float top = m, ref = M;
         uint32_t z0[32], z1[32];
-        // (the next 32 scores are on their way from tensor memory meanwhile)
-        auto largest = [&](uint32_t (&z)[32], int g) {
-          const int src = (32 * g) >> shift;
-          const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
-          const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
-          const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
-          if (masked) mask(z, g, key0, pid >= 0);
-          const float pm = max32(z) * c;
-          top = fmaxf(top, pm);
-          ref = fmaxf(ref, pm + fmaxf(lv, -126.f) - 10.f);
-        };
-        tc::ld32_nowait(sc, z0);
-        tc::ld_wait32(z0);
-#pragma unroll 1
-        for (int g = 0; g < 4; g += 2) {
-          tc::ld32_nowait(sc + 32 * g + 32, z1);
-          largest(z0, g);
-          tc::ld_wait32(z1);
-          tc::ld32_nowait(sc + (32 * g + 64) % 128, z0);  // at the end: for the next pass
-          largest(z1, g + 1);
+        if (!masked) {
+          // (the next 32 scores are on their way from tensor memory meanwhile)
+          tc::ld32_nowait(sc, z0);
           tc::ld_wait32(z0);
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            tc::ld32_nowait(sc + 32 * g + 32, z1);
+            largest(z0, c[g], lv[g], top, ref);
+            tc::ld_wait32(z1);
+            tc::ld32_nowait(sc + (32 * g + 64) % 128, z0);  // at the end: for the weights
+            largest(z1, c[g + 1], lv[g + 1], top, ref);
+            tc::ld_wait32(z0);
+          }
+        } else {
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            uint32_t y[16];
+            tc::ld16_sync(sc + 16 * g, y);
+            const int src = (16 * g) >> shift;
+            const float cg = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
+            const float lg = __shfl_sync(0xffffffffu, pg.lv, src);
+            const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
+            const int from = pid >= 0 ? lo - key0 - 16 * g : 16, to = hi - key0 - 16 * g;
+            float x = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= from && e < to) x = fmaxf(x, __uint_as_float(y[e]));
+            x *= cg;
+            top = fmaxf(top, x);
+            ref = fmaxf(ref, x + fmaxf(lg, -126.f) - 10.f);
+          }
         }
         next.scales(a, w.at.h);  // on their way during the exponentials
         const float base = top == -INFINITY ? 0.f : top;
@@ -534,60 +614,39 @@ struct Softmax {
           }
         }
         const float oref = M == -INFINITY ? 0.f : M;
-        const int least = __reduce_min_sync(
-            0xffffffffu, lane < CK >> shift && pg.pid >= 0 ? __float2int_rd(pg.lv) : INT_MAX);
         const bool apart = __any_sync(
             0xffffffffu, fabsf(base) > 4194304.f || !(base - oref + (float)least > -60.f));
         float sum = 0.f;
-        if (!apart) {
-          auto weights = [&](uint32_t (&z)[32], int g) {
-            const int src = (32 * g) >> shift;
-            const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
-            const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
-            const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
-            if (masked) mask(z, g, key0, pid >= 0);
-            const float off = pid >= 0 ? lv - oref : 0.f;
-            float s0 = 0.f, s1 = 0.f;
-            uint32_t p[16];
+        if (!masked && !apart) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float p0 = ptx::ex2(fmaf(__uint_as_float(z[2 * e]), c, off));
-              const float p1 = ptx::ex2(fmaf(__uint_as_float(z[2 * e + 1]), c, off));
-              s0 += p0;
-              s1 += p1;
-              p[e] = pack_half(p0, p1);
-            }
-            tc::st16(sc + 16 * g, p);  // over scores that are read already
-            if (pid >= 0) sum = fmaf(s0 + s1, ptx::ex2(oref - base - lv), sum);
-          };
-#pragma unroll 1
           for (int g = 0; g < 4; g += 2) {
             tc::ld32_nowait(sc + 32 * g + 32, z1);
-            weights(z0, g);
+            weights(z0, sc + 16 * g, c[g], lv[g], oref, base, sum);
             tc::ld_wait32(z1);
             if (g == 0) tc::ld32_nowait(sc + 64, z0);
-            weights(z1, g + 1);
+            weights(z1, sc + 16 * g + 16, c[g + 1], lv[g + 1], oref, base, sum);
             if (g == 0) tc::ld_wait32(z0);
           }
         } else {
-          // p for itself, from a rounded score (see q8_attend.cu)
+          // keys that the row does not see; and p for itself, from a rounded
+          // score (see q8_attend.cu)
 #pragma unroll 1
           for (int g = 0; g < 8; ++g) {
             const int src = (16 * g) >> shift;
-            const float c = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
-            const float lv = __shfl_sync(0xffffffffu, pg.lv, src);
+            const float cg = fmaxf(qf * __shfl_sync(0xffffffffu, pg.ks, src), 1.17549435e-38f);
+            const float lg = __shfl_sync(0xffffffffu, pg.lv, src);
             const int pid = __shfl_sync(0xffffffffu, pg.pid, src);
             uint32_t y[16], p[8];
             tc::ld16_sync(sc + 16 * g, y);
-            const float off = pid >= 0 ? base - oref + lv : 0.f;
+            const int from = pid >= 0 ? lo - key0 - 16 * g : 16, to = hi - key0 - 16 * g;
+            const float off = pid >= 0 ? base - oref + lg : 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               float r[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int key = key0 + 16 * g + e + k;
-                const float d = __fadd_rn(__fmul_rn(__uint_as_float(y[e + k]), c), -base);
-                const bool seen = pid >= 0 && key >= lo && key < hi;
+                const float d = __fadd_rn(__fmul_rn(__uint_as_float(y[e + k]), cg), -base);
+                const bool seen = e + k >= from && e + k < to;
                 sum += seen ? ptx::ex2(d) : 0.f;
                 r[k] = seen ? ptx::ex2(d + off) : 0.f;
               }
@@ -656,13 +715,7 @@ struct Softmax {
         mm[cta].unit = (long)w.at.tile * a.Hkv + w.at.h;
         mm[cta].from = q8::block_of(u0, V, C);
       }
-      if (nan) {  // (the same for every row of the unit) the marks are used up
-        const int threads = u.rows > 128 ? 256 : 128;
-        ptx::named_bar_sync(1, threads);
-        for (int k = 128 * t + row; k < D * 8; k += threads) (&sm.nan_rows[slot][0][0])[k] = 0;
-        if (t == 0 && row == 0) B.nan_flag[slot] = 0;
-        ptx::named_bar_sync(1, threads);
-      }
+      use_marks(u, slot);
     }
   }
 };
@@ -714,16 +767,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (cta < C && V > 0) {
     const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
     const int shift = __ffs(a.page) - 1;
+    // the launch's 128 registers a thread, dealt to the warpgroups anew:
+    // 2 * 192 + 80 + 48 = 4 * 128
     if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
       Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane,
                 B.tmem + ((uint32_t)((warp & 3) * 32) << 16), shift, 0.f, 0, 0};
       s.run(pl, X0, X1, cta, V, C);
     } else if (warp < 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       Converter{a, warp - 8, lane, shift}.run(pl, X0, X1, sm);
-    } else if (warp == 13) {
-      copy_pages(a, pl, X0, X1, sm, shift, lane);
-    } else if (lane == 0) {
-      issue_mmas(a, pl, X0, X1, sm);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      if (warp == 13)
+        copy_pages(a, pl, X0, X1, sm, shift, lane);
+      else if (warp == 12 && lane == 0)
+        issue_mmas(a, pl, X0, X1, sm);
     }
   }
   tc::fence_before_sync();
