@@ -44,7 +44,9 @@ constexpr float kLag = 5.f;        // how far M may fall behind before O is resc
 constexpr int kRing = 3;           // fp16 tiles: K of chunk 0, V of it, K of chunk 1, ...
 constexpr int kRaw = 3;            // tiles of codes under way
 constexpr int kNanSlots = 4;       // units whose NaN marks are under way
-constexpr long kPart = (long)ROWS * D + ROWS;  // floats of a partial: o, lse2
+// Floats of a partial: o as [D / 4][ROWS] of 4 components (a thread has a row: a
+// warp's stores are contiguous), then lse2 of the rows.
+constexpr long kPart = (long)ROWS * D + ROWS;
 
 // Tensor-memory columns of half t: S, later P; and O.
 __device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
@@ -70,6 +72,7 @@ struct Smem {
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                      unsigned* err) {
+  if (ptx::mbar_try_wait(bar, parity & 1u)) return true;
   if (*abort) return false;
   if (ptx::mbar_wait(bar, parity & 1u, kWaitNs)) return true;
   atomicOr(err, kErrTimeout);
@@ -108,6 +111,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 16 components as bf16: a 32-byte sector in two stores.
+__device__ __forceinline__ void store32(__nv_bfloat16* dst, const float* y) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16(y[2 * i], y[2 * i + 1]);
+  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // A unit: a tile's rows of one KV head.
@@ -364,7 +376,8 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
     for (int t = 0; t < halves; ++t) qk(t, n);
     for (int i = 0; ok && i < w.n; ++i, n += 2) {
       const bool more = i + 1 < w.n;
-      ok = ready(n + 1);
+      // (both are converted ahead; no wait then lies between the products but P's)
+      ok = ready(n + 1) && (!more || ready(n + 2));
       for (int t = 0; ok && t < halves; ++t) {
         ok = wait(&B.p_full[t], tiles[t]++, abort, a.err);
         if (!ok) break;
@@ -378,8 +391,7 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
         if (!more) {
           tc::commit(&B.o_full[t]);
         } else {
-          if (t == 0) ok = ready(n + 2);
-          if (ok) qk(t, n + 2);
+          qk(t, n + 2);
         }
       }
     }
@@ -694,14 +706,12 @@ struct Softmax {
         }
         if (whole) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            reinterpret_cast<uint4*>(dst + 32 * q4)[e / 8] =
-                make_uint4(ptx::pack_bf16(y[e], y[e + 1]), ptx::pack_bf16(y[e + 2], y[e + 3]),
-                           ptx::pack_bf16(y[e + 4], y[e + 5]), ptx::pack_bf16(y[e + 6], y[e + 7]));
+          for (int e = 0; e < 32; e += 16) store32(dst + 32 * q4 + e, &y[e]);
         } else {
-          float4* to = reinterpret_cast<float4*>(part + (long)(128 * t + row) * D + 32 * q4);
+          float4* to = reinterpret_cast<float4*>(part) + 8 * q4 * ROWS + 128 * t + row;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            to[e * ROWS] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
         }
       }
       if (real) {
@@ -791,15 +801,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 12) tc::tmem_dealloc(B.tmem, 512);
 }
 
-// Joins the partials of a unit that lies in several blocks: a warp per row of
-// the unit that ends in attention block blockIdx.x (see q8_attend.cuh).
-constexpr int kMergeWarps = 8;
-__global__ void __launch_bounds__(32 * kMergeWarps)
+// Joins the partials of a unit that lies in several blocks (see q8_attend.cuh):
+// block (c, y) does components 16 y .. 16 y + 15 of the unit that ends in
+// attention block c, a thread per row.
+constexpr int kMergeCols = 16;
+__global__ void __launch_bounds__(ROWS)
     q8_prefill_tc_merge_kernel(const __grid_constant__ Q8AttendArgs a) {
   ptx::grid_dep_wait();
   const q8::MergeMeta mm = reinterpret_cast<const q8::MergeMeta*>(a.meta)[blockIdx.x];
   if (mm.unit < 0) return;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int row = threadIdx.x, col = kMergeCols * blockIdx.y;
   const int tile = (int)(mm.unit / a.Hkv), h = (int)(mm.unit % a.Hkv);
   const int b = a.plan_seq[tile];
   const int r = (tile - a.plan_base[b]) * ROWS + row;
@@ -809,27 +820,30 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   const int np = (int)blockIdx.x - mm.from + 1;
   auto part = [&](int i) { return a.part + (2l * (mm.from + i) + (i == 0 ? 1 : 0)) * kPart; };
   float top = -INFINITY;
-  for (int i = lane; i < np; i += 32) top = fmaxf(top, part(i)[(long)ROWS * D + row]);
-  top = warp_max(top);
-  const float base = top == -INFINITY ? 0.f : top;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
 #pragma unroll 4
+  for (int i = 0; i < np; ++i) top = fmaxf(top, part(i)[(long)ROWS * D + row]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float acc[kMergeCols] = {}, sum = 0.f;
+#pragma unroll 2
   for (int i = 0; i < np; ++i) {
     const float* p = part(i);
     const float w = ptx::ex2(p[(long)ROWS * D + row] - base);
-    const float4 x = reinterpret_cast<const float4*>(p + (long)row * D)[lane];
     sum += w;
-    acc.x = fmaf(w, x.x, acc.x);
-    acc.y = fmaf(w, x.y, acc.y);
-    acc.z = fmaf(w, x.z, acc.z);
-    acc.w = fmaf(w, x.w, acc.w);
+#pragma unroll
+    for (int e = 0; e < kMergeCols / 4; ++e) {
+      const float4 x = reinterpret_cast<const float4*>(p)[(col / 4 + e) * ROWS + row];
+      acc[4 * e] = fmaf(w, x.x, acc[4 * e]);
+      acc[4 * e + 1] = fmaf(w, x.y, acc[4 * e + 1]);
+      acc[4 * e + 2] = fmaf(w, x.z, acc[4 * e + 2]);
+      acc[4 * e + 3] = fmaf(w, x.w, acc[4 * e + 3]);
+    }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < kMergeCols; ++e) acc[e] *= f;
   const long out = ((long)first + r / a.G) * a.Hq + h * a.G + r % a.G;
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out * D)[lane] =
-      make_uint2(ptx::pack_bf16(acc.x * f, acc.y * f), ptx::pack_bf16(acc.z * f, acc.w * f));
-  if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * q8::kLn2;
+  store32(static_cast<__nv_bfloat16*>(a.out) + out * D + col, acc);
+  if (col == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * q8::kLn2;
 }
 
 }  // namespace
@@ -851,8 +865,8 @@ cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, cudaStream_t stream) {
       return e;
   }
   TraceScope trace("q8_prefill_tc_merge", stream);
-  return q8::launch_pdl(q8_prefill_tc_merge_kernel, dim3(a.blocks, ROWS / kMergeWarps),
-                        dim3(32 * kMergeWarps), 0, stream, a);
+  return q8::launch_pdl(q8_prefill_tc_merge_kernel, dim3(a.blocks, D / kMergeCols),
+                        dim3(ROWS), 0, stream, a);
 }
 
 }  // namespace nsa
