@@ -202,8 +202,8 @@ struct Q8AttendArgs {
 };
 // Chunks of queries on the tensor memory (q8_prefill_tc.cu): bf16, d = 128,
 // pages of 32 tokens or more. The plan is made by the caller, for tiles of
-// kQ8TcRows rows and chunks of kQ8TcKeys keys.
-constexpr int kQ8TcRows = 256, kQ8TcKeys = 128;
+// kQ8TcRows rows and chunks of kQ8TcKeys keys, kQ8TcUnit chunks more a unit.
+constexpr int kQ8TcRows = 256, kQ8TcKeys = 128, kQ8TcUnit = 8;
 bool q8_prefill_tc_shape(const nsa_params& p);
 size_t q8_prefill_tc_part_bytes();
 cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, cudaStream_t stream);

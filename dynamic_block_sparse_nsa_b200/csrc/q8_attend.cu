@@ -1061,7 +1061,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 }
 
 // The plan of a call with offsets, or of more tiles than a block takes in: the
-// tiles of every sequence and the chunks before each tile. One block.
+// tiles of every sequence and the chunks before each tile, `extra` for a unit's own
+// cost included. One block.
 constexpr int kPlanThreads = 1024;
 template <typename I>
 __device__ __forceinline__ I block_scan(I mine, I* sums, I& total) {
@@ -1085,7 +1086,7 @@ __device__ __forceinline__ I block_scan(I mine, I* sums, I& total) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArgs a, int tile_rows,
-                                                               int chunk) {
+                                                               int chunk, int extra) {
   __shared__ long sums[kPlanThreads / 32];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -1124,7 +1125,8 @@ __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArg
       }
       a.plan_seq[t] = b;
       const Seq s = q8::sequence(a, b);
-      mine = (long)q8::chunks_of(a, s, (t - a.plan_base[b]) * tile_rows, tile_rows, chunk) * a.Hkv;
+      mine = (long)(q8::chunks_of(a, s, (t - a.plan_base[b]) * tile_rows, tile_rows, chunk) + extra) *
+             a.Hkv;
     }
     const long at = block_scan(mine, sums, all);
     if (t < tiles) a.plan_pre[t + 1] = base + at + mine;
@@ -1222,7 +1224,7 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
     a.plan_base = reinterpret_cast<int*>(w + L.base);
     TraceScope trace("q8_plan", stream);
     const cudaError_t e = q8::launch_pdl(q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a,
-                                         tc ? kQ8TcRows : ROWS, tc ? kQ8TcKeys : CK);
+                                         tc ? kQ8TcRows : ROWS, tc ? kQ8TcKeys : CK, tc ? kQ8TcUnit : 0);
     if (e != cudaSuccess) return e;
   }
   if (tc) return launch_q8_prefill_tc(a, stream);

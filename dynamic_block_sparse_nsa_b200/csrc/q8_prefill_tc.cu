@@ -38,7 +38,7 @@ constexpr int ROWS = kQ8TcRows;
 constexpr int CK = kQ8TcKeys;
 constexpr uint32_t ATOM = 16384;   // 128 rows x 64 halves
 constexpr uint32_t TILE = 32768;   // 128 rows x 128 halves
-constexpr int kThreads = 16 * 32;  // (warps 14 and 15 only give registers away)
+constexpr int kThreads = 14 * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLag = 5.f;        // how far M may fall behind before O is rescaled
 constexpr int kRing = 3;           // fp16 tiles: K of chunk 0, V of it, K of chunk 1, ...
@@ -143,32 +143,47 @@ struct Unit {
   }
 };
 
-// The block's chunks, unit by unit: `n` chunks of the current unit from `at.c` on.
+// The block's chunks, unit by unit: `n` chunks of the current unit from its
+// chunk `first` on. The plan counts a unit's own cost (query rows in, output
+// rows out) as kQ8TcUnit chunks ahead of its real ones.
 struct Walk {
   Place at;
   Unit u;
   long x, end;
-  int n, seg;
+  int first, n, seg;
   __device__ __forceinline__ void start(const Q8AttendArgs& a, const Plan& pl, long x0, long x1) {
     x = x0;
     end = x1;
     seg = 0;
     at.init(pl, a.Hkv, x0);
     u.load(a, pl, at.tile);
-    n = (int)min((long)(at.nc - at.c), x1 - x0);
+    settle(a, pl);
   }
-  __device__ __forceinline__ bool done() const { return x >= end; }
-  __device__ __forceinline__ void next(const Q8AttendArgs& a, const Plan& pl) {
-    x += n;
-    ++seg;
+  __device__ __forceinline__ int span() const { return (int)min((long)(at.nc - at.c), end - x); }
+  __device__ __forceinline__ void settle(const Q8AttendArgs& a, const Plan& pl) {
+    while (x < end) {
+      first = max(0, at.c - kQ8TcUnit);
+      n = at.c + span() - kQ8TcUnit - first;
+      if (n > 0) return;
+      step(a, pl);
+    }
+  }
+  __device__ __forceinline__ void step(const Q8AttendArgs& a, const Plan& pl) {
+    x += span();
     if (x >= end) return;
     const int tile = at.tile;
     at.c = at.nc - 1;  // (only a unit's last segment is followed by another)
     at.next(pl, a.Hkv);
     if (at.tile != tile) u.load(a, pl, at.tile);
-    n = (int)min((long)at.nc, end - x);
   }
-  __device__ __forceinline__ int key0(int i) const { return (u.lo / CK + at.c + i) * CK; }
+  __device__ __forceinline__ bool done() const { return x >= end; }
+  __device__ __forceinline__ void next(const Q8AttendArgs& a, const Plan& pl) {
+    ++seg;
+    step(a, pl);
+    settle(a, pl);
+  }
+  __device__ __forceinline__ int key0(int i) const { return (u.lo / CK + first + i) * CK; }
+  __device__ __forceinline__ bool ends() const { return first + n == at.nc - kQ8TcUnit; }
 };
 
 // Lane j's page of the chunk that begins at key0 (j < 128 / page); -1: none,
@@ -187,42 +202,40 @@ __device__ void copy_pages(const Q8AttendArgs& a, const Plan& pl, long X0, long 
                            int shift, int lane) {
   Bars& B = sm.bars;
   volatile int* abort = &B.abort;
-  const int chunks = (int)(X1 - X0);
   const uint32_t bytes = (uint32_t)D << shift;
   Walk w;
-  w.start(a, pl, X0, X1);
-  int i = 0;
-  int pid = page_of(a, w.u, w.key0(0), lane, shift);  // lane j: page j of the chunk
   bool ok = true;
-  int n = 0;
-  for (int j = 0; ok && j < chunks; ++j) {
-    if (pid >= a.num_pages) {
-      atomicOr(a.err, kErrPage);
-      pid = -1;
-    }
-    const bool mine = pid >= 0;
-    const uint32_t live = __ballot_sync(0xffffffffu, mine);
-    const long from = ((long)pid * a.Hkv + w.at.h) << (shift + 7);
-    if (++i == w.n) {
-      w.next(a, pl);
-      i = 0;
-    }
-    pid = w.done() ? -1 : page_of(a, w.u, w.key0(i), lane, shift);
-    for (int v = 0; ok && v < 2; ++v, ++n) {
-      const int r = n % kRaw;
-      if (n >= kRaw) ok = wait(&B.raw_empty[r], n / kRaw - 1, abort, a.err);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+  int n = 0;  // the block's tile
+  for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
+    const int chunks = w.n;
+    int key0 = w.key0(0);
+    int pid = page_of(a, w.u, key0, lane, shift);  // lane j: page j of the chunk
+    for (int i = 0; ok && i < chunks; ++i) {
+      if (pid >= a.num_pages) {
+        atomicOr(a.err, kErrPage);
+        pid = -1;
       }
-      if (lane == 0) {
-        B.live[r] = live;
-        ptx::mbar_arrive_expect_tx(&B.raw_full[r], __popc(live) * bytes);
+      const bool mine = pid >= 0;
+      const uint32_t live = __ballot_sync(0xffffffffu, mine);
+      const long from = ((long)pid * a.Hkv + w.at.h) << (shift + 7);
+      key0 += CK;
+      pid = page_of(a, w.u, key0, lane, shift);  // the next chunk's, ahead
+      for (int v = 0; ok && v < 2; ++v, ++n) {
+        const int r = n % kRaw;
+        if (n >= kRaw) ok = wait(&B.raw_empty[r], n / kRaw - 1, abort, a.err);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          B.live[r] = live;
+          ptx::mbar_arrive_expect_tx(&B.raw_full[r], __popc(live) * bytes);
+        }
+        __syncwarp();
+        if (mine)
+          ptx::bulk_load(sm.raw[r] + lane * bytes, (v ? a.v_pages : a.k_pages) + from, bytes,
+                         &B.raw_full[r]);
       }
-      __syncwarp();
-      if (mine)
-        ptx::bulk_load(sm.raw[r] + lane * bytes, (v ? a.v_pages : a.k_pages) + from, bytes,
-                       &B.raw_full[r]);
     }
   }
   // every copy has landed before the block ends
@@ -301,41 +314,41 @@ struct Converter {
   __device__ void run(const Plan& pl, long X0, long X1, Smem& sm) const {
     Bars& B = sm.bars;
     volatile int* abort = &B.abort;
-    const int tiles = 2 * (int)(X1 - X0);
     Walk w;
-    w.start(a, pl, X0, X1);
-    int i = 0;
+    int n = 0;  // the block's tile
 #pragma unroll 1
-    for (int n = 0; n < tiles; ++n) {
-      const int r = n % kRaw, buf = n % kRing;
-      wait(&B.raw_full[r], n / kRaw, abort, a.err);
-      const uint32_t live = B.live[r];
-      uint4 x[8];
+    for (w.start(a, pl, X0, X1); !w.done(); w.next(a, pl)) {
+      const int lo = w.u.lo, hi = w.u.hi, all_lo = w.u.all_lo, all_hi = w.u.all_hi;
+      const int slot = w.seg % kNanSlots, tiles = 2 * w.n;
+      int key0 = w.key0(0);
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i, ++n) {
+        const int r = n % kRaw, buf = n % kRing;
+        wait(&B.raw_full[r], n / kRaw, abort, a.err);
+        const uint32_t live = B.live[r];
+        uint4 x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        x[k] = *reinterpret_cast<const uint4*>(sm.raw[r] + row(k) * D + (lane & 7) * 16);
-      ptx::mbar_arrive(&B.raw_empty[r]);
-      const int key0 = w.key0(i);
-      if (key0 + CK > w.u.all_hi || key0 < w.u.all_lo || live != (1u << (CK >> shift)) - 1) {
-        // rows that no token sees hold anything: zeros
+        for (int k = 0; k < 8; ++k)
+          x[k] = *reinterpret_cast<const uint4*>(sm.raw[r] + row(k) * D + (lane & 7) * 16);
+        ptx::mbar_arrive(&B.raw_empty[r]);
+        if (key0 + CK > all_hi || key0 < all_lo || live != (1u << (CK >> shift)) - 1) {
+          // rows that no token sees hold anything: zeros
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int pos = key0 + row(k);
-          if (pos < w.u.lo || pos >= w.u.hi || !(live >> (row(k) >> shift) & 1u))
-            x[k] = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 8; ++k) {
+            const int pos = key0 + row(k);
+            if (pos < lo || pos >= hi || !(live >> (row(k) >> shift) & 1u))
+              x[k] = make_uint4(0, 0, 0, 0);
+          }
+          if (i & 1)
+            mark_nan(x, w.u.s.len - w.u.s.n + w.u.tok0, w.u.tok1 - w.u.tok0, key0,
+                     sm.nan_rows[slot], &B.nan_flag[slot]);
         }
-        if (n & 1)
-          mark_nan(x, w.u.s.len - w.u.s.n + w.u.tok0, w.u.tok1 - w.u.tok0, key0,
-                   sm.nan_rows[w.seg % kNanSlots], &B.nan_flag[w.seg % kNanSlots]);
+        if (n >= kRing) wait(&B.empty[buf], n / kRing - 1, abort, a.err);
+        store(x, sm.kv[buf]);
+        ptx::fence_proxy_async();
+        ptx::mbar_arrive(&B.full[buf]);
+        if (i & 1) key0 += CK;
       }
-      if ((n & 1) && ++i == w.n) {
-        w.next(a, pl);
-        i = 0;
-      }
-      if (n >= kRing) wait(&B.empty[buf], n / kRing - 1, abort, a.err);
-      store(x, sm.kv[buf]);
-      ptx::fence_proxy_async();
-      ptx::mbar_arrive(&B.full[buf]);
     }
   }
 };
@@ -356,7 +369,7 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
   bool ok = true;
   int n = 0;  // the block's K tile (its V tile is n + 1)
   for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
-    const int halves = w.u.rows > 128 ? 2 : 1;
+    const int halves = w.u.rows > 128 ? 2 : 1, chunks = w.n;
     auto ready = [&](int k) {
       const bool r = wait(&B.full[k % kRing], k / kRing, abort, a.err);
       tc::fence_after_sync();
@@ -374,8 +387,8 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
     ok = ok && ready(n);
     if (!ok) break;
     for (int t = 0; t < halves; ++t) qk(t, n);
-    for (int i = 0; ok && i < w.n; ++i, n += 2) {
-      const bool more = i + 1 < w.n;
+    for (int i = 0; ok && i < chunks; ++i, n += 2) {
+      const bool more = i + 1 < chunks;
       // (both are converted ahead; no wait then lies between the products but P's)
       ok = ready(n + 1) && (!more || ready(n + 2));
       for (int t = 0; ok && t < halves; ++t) {
@@ -550,12 +563,13 @@ struct Softmax {
         continue;
       }
       float m = -INFINITY, M = -INFINITY, l = 0.f;
-      Pages pg{page_of(a, u, w.key0(0), lane, shift), 0.f, 0.f, 0.f};
-      pg.scales(a, w.at.h);
+      const int chunks = w.n, h = w.at.h;
+      int key0 = w.key0(0);
+      Pages pg{page_of(a, u, key0, lane, shift), 0.f, 0.f, 0.f};
+      pg.scales(a, h);
 #pragma unroll 1
-      for (int i = 0; i < w.n; ++i) {
-        const int key0 = w.key0(i);
-        Pages next{i + 1 < w.n ? page_of(a, u, key0 + CK, lane, shift) : -1, 0.f, 0.f, 0.f};
+      for (int i = 0; i < chunks; ++i, key0 += CK) {
+        Pages next{page_of(a, u, key0 + CK, lane, shift), 0.f, 0.f, 0.f};
         pg.lv = __log2f(pg.vs);
         const bool mine = lane < CK >> shift;
         const bool masked = __any_sync(
@@ -605,7 +619,7 @@ struct Softmax {
             ref = fmaxf(ref, x + fmaxf(lg, -126.f) - 10.f);
           }
         }
-        next.scales(a, w.at.h);  // on their way during the exponentials
+        next.scales(a, h);  // on their way during the exponentials
         const float base = top == -INFINITY ? 0.f : top;
         l *= ptx::ex2(m - base);
         m = top;
@@ -679,15 +693,14 @@ struct Softmax {
       tc::fence_after_sync();
       const int r = u.r0 + 128 * t + row;
       const bool real = r < u.s.n * a.G;
-      const long u0 = w.x - w.at.c;
-      const bool whole = u0 >= X0 && u0 + w.at.nc <= X1;
+      const bool whole = w.first == 0 && w.ends();
       const float base = m == -INFINITY ? 0.f : m, oref = M == -INFINITY ? 0.f : M;
       // in two factors: 2^(M - m) alone can leave fp32's range
       const float half = ptx::ex2(0.5f * (oref - base)), f = l == 0.f ? 0.f : half / l;
       const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
       const int slot = w.seg % kNanSlots;
       const bool nan = *(volatile int*)&B.nan_flag[slot] != 0;
-      float* part = a.part + (2l * cta + (u0 < X0 ? 0 : 1)) * kPart;
+      float* part = a.part + (2l * cta + (w.first > 0 ? 0 : 1)) * kPart;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (real ? out_row(u, w.at.h, r) : 0) * D;
 #pragma unroll 1
       for (int q4 = 0; q4 < 4; ++q4) {
@@ -721,9 +734,9 @@ struct Softmax {
           part[(long)ROWS * D + 128 * t + row] = lse2;
         }
       }
-      if (t == 0 && row == 0 && !whole && u0 < X0 && u0 + w.at.nc <= X1) {
+      if (t == 0 && row == 0 && w.first > 0 && w.ends()) {
         mm[cta].unit = (long)w.at.tile * a.Hkv + w.at.h;
-        mm[cta].from = q8::block_of(u0, V, C);
+        mm[cta].from = q8::block_of(w.x - w.at.c + kQ8TcUnit, V, C);
       }
       use_marks(u, slot);
     }
@@ -777,22 +790,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (cta < C && V > 0) {
     const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
     const int shift = __ffs(a.page) - 1;
-    // the launch's 128 registers a thread, dealt to the warpgroups anew:
-    // 2 * 192 + 80 + 48 = 4 * 128
     if (warp < 8) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
       Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane,
                 B.tmem + ((uint32_t)((warp & 3) * 32) << 16), shift, 0.f, 0, 0};
       s.run(pl, X0, X1, cta, V, C);
     } else if (warp < 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       Converter{a, warp - 8, lane, shift}.run(pl, X0, X1, sm);
-    } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-      if (warp == 13)
-        copy_pages(a, pl, X0, X1, sm, shift, lane);
-      else if (warp == 12 && lane == 0)
-        issue_mmas(a, pl, X0, X1, sm);
+    } else if (warp == 13) {
+      copy_pages(a, pl, X0, X1, sm, shift, lane);
+    } else if (lane == 0) {
+      issue_mmas(a, pl, X0, X1, sm);
     }
   }
   tc::fence_before_sync();
