@@ -49,17 +49,23 @@ __device__ __forceinline__ int scale_exponent(float a) {
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <typename T>
-struct Vec8;  // 8 elements, 16-byte accesses
+struct Vec8;  // 8 elements, 16-byte accesses; Raw: as they are in memory
 template <>
 struct Vec8<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw load_raw(const __nv_bfloat16* p) {
+    return __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  static __device__ __forceinline__ void unpack(const Raw& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+  }
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
+    unpack(load_raw(p), x);
   }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
     uint32_t w[4];
@@ -73,6 +79,17 @@ struct Vec8<__nv_bfloat16> {
 };
 template <>
 struct Vec8<float> {
+  struct Raw {
+    float4 a, b;
+  };
+  static __device__ __forceinline__ Raw load_raw(const float* p) {
+    const float4* q = reinterpret_cast<const float4*>(p);
+    return Raw{__ldg(q), __ldg(q + 1)};
+  }
+  static __device__ __forceinline__ void unpack(const Raw& v, float* x) {
+    *reinterpret_cast<float4*>(x) = v.a;
+    *reinterpret_cast<float4*>(x + 4) = v.b;
+  }
   static __device__ __forceinline__ void load(const float* p, float* x) {
     *reinterpret_cast<float4*>(x) = __ldg(reinterpret_cast<const float4*>(p));
     *reinterpret_cast<float4*>(x + 4) = __ldg(reinterpret_cast<const float4*>(p) + 1);

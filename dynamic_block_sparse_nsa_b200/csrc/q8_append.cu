@@ -14,9 +14,11 @@
 // Bound by bytes (each input read once, each output written once) for long
 // calls and by latency for one token per sequence. A (page, head) of K or V is
 // one block's work: its rows stay in registers between the maximum and the
-// codes, so nothing is read twice; blocks behind those rotate query rows. With
+// codes, so nothing is read from memory twice; blocks behind those rotate query rows. With
 // one token per sequence a warp takes a (sequence, head) of K or V instead.
-#include "q8.cuh"
+#include <algorithm>
+
+#include "q8_attend.cuh"
 
 namespace nsa {
 namespace {
@@ -38,37 +40,41 @@ __device__ __forceinline__ void pieces(int j, int rot, int& a, int& b) {
   }
 }
 
-// Rotates the 16 components x = [piece a, piece b] of a row by table row
-// rope[rot] = [cos | sin].
-__device__ __forceinline__ void rotate(float (&x)[16], const float* rope, int rot, int style,
-                                       int j) {
-  if (j >= rot / 16) return;
-  const float* cs = rope;
-  const float* sn = rope + rot / 2;
-  if (style == NSA_ROPE_HALF) {
-    float c[8], s[8];
-    Vec8<float>::load(cs + 8 * j, c);
-    Vec8<float>::load(sn + 8 * j, s);
+// Cosines [8] and sines [8] of a row's pieces at a position: with pairs
+// (i, i + rot / 2) those of pairs 8 j .., with pairs (2i, 2i + 1) those of
+// 4 j .. 4 j + 3 (piece a) and rot / 4 + 4 j .. (piece b).
+template <bool HALF>
+__device__ __forceinline__ void turn_of(float (&cs)[16], const Q8AppendArgs& a, int at, int j) {
+  if (j >= a.rot / 16) return;
+  const float* row = a.rope + (long)at * a.rot;
+  const int p0 = HALF ? 8 * j : 4 * j;
+  const int p1 = HALF ? 8 * j + 4 : a.rot / 4 + 4 * j;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float* from = row + k * (a.rot / 2);
+    *reinterpret_cast<float4*>(&cs[8 * k]) = __ldg(reinterpret_cast<const float4*>(from + p0));
+    *reinterpret_cast<float4*>(&cs[8 * k + 4]) = __ldg(reinterpret_cast<const float4*>(from + p1));
+  }
+}
+
+// Rotates the 16 components x = [piece a, piece b] of a row.
+template <bool HALF>
+__device__ __forceinline__ void rotate(float (&x)[16], const float (&cs)[16],
+                                       const Q8AppendArgs& a, int j) {
+  if (j >= a.rot / 16) return;
+  if (HALF) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float u = x[i], v = x[8 + i];
-      x[i] = u * c[i] - v * s[i];
-      x[8 + i] = v * c[i] + u * s[i];
+      x[i] = u * cs[i] - v * cs[8 + i];
+      x[8 + i] = v * cs[i] + u * cs[8 + i];
     }
   } else {
-    // pairs 4j .. 4j + 3 in piece a, rot / 4 + 4j .. in piece b
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = (h ? rot / 4 : 0) + 4 * j;
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + at));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(sn + at));
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = x[8 * h + 2 * i], v = x[8 * h + 2 * i + 1];
-        x[8 * h + 2 * i] = u * cc[i] - v * ss[i];
-        x[8 * h + 2 * i + 1] = v * cc[i] + u * ss[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float u = x[2 * i], v = x[2 * i + 1];
+      x[2 * i] = u * cs[i] - v * cs[8 + i];
+      x[2 * i + 1] = v * cs[i] + u * cs[8 + i];
     }
   }
 }
@@ -146,16 +152,17 @@ __device__ __forceinline__ bool place_ok(const Q8AppendArgs& a, int pos, int n) 
   return pos >= 0 && (long)pos + n <= a.T && (a.rot == 0 || (long)pos + n <= a.rope_len);
 }
 
-// A row of the queries: rotated into q_out.
-template <typename T>
+// A row of the queries, at position `at`, rotated into q_out.
+template <typename T, bool HALF>
 __device__ __forceinline__ void turn_query(const Q8AppendArgs& a, long row, int at, int j) {
   int pa, pb;
   pieces(j, a.rot, pa, pb);
   const T* src = static_cast<const T*>(a.q) + row * a.d;
-  float x[16];
+  float x[16], cs[16];
   Vec8<T>::load(src + pa, x);
   Vec8<T>::load(src + pb, x + 8);
-  rotate(x, a.rope + (long)at * a.rot, a.rot, a.style, j);
+  turn_of<HALF>(cs, a, at, j);
+  rotate<HALF>(x, cs, a, j);
   T* dst = static_cast<T*>(a.q_out) + row * a.d;
   Vec8<T>::store(dst + pa, x);
   Vec8<T>::store(dst + pb, x + 8);
@@ -163,7 +170,7 @@ __device__ __forceinline__ void turn_query(const Q8AppendArgs& a, long row, int 
 
 // One token per sequence: a warp per (sequence, KV head, K or V), then warps
 // that take 32 / (d / 16) query rows each.
-template <typename T>
+template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) q8_append_step_kernel(Q8AppendArgs a) {
   const int lane = threadIdx.x & 31;
   const long w = blockIdx.x * (long)(kThreads / 32) + (threadIdx.x >> 5);
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) q8_append_step_kernel(Q8AppendArgs a
     const long row = (w - items) * (32 / tpr) + lane / tpr;
     if (!a.q || row >= (long)a.B * a.Hq) return;
     const int pos = a.pos[row / a.Hq];
-    if (place_ok(a, pos, 1)) turn_query<T>(a, row, pos, lane % tpr);
+    if (place_ok(a, pos, 1)) turn_query<T, HALF>(a, row, pos, lane % tpr);
     return;
   }
   const int isv = (int)(w & 1), h = (int)((w >> 1) % a.Hkv), b = (int)((w >> 1) / a.Hkv);
@@ -201,7 +208,11 @@ __global__ void __launch_bounds__(kThreads) q8_append_step_kernel(Q8AppendArgs a
     const T* src = static_cast<const T*>(isv ? a.v_new : a.k_new) + row * a.d;
     Vec8<T>::load(src + pa, x);
     Vec8<T>::load(src + pb, x + 8);
-    if (!isv) rotate(x, a.rope + (long)pos * a.rot, a.rot, a.style, lane);
+    if (!isv) {
+      float cs[16];
+      turn_of<HALF>(cs, a, pos, lane);
+      rotate<HALF>(x, cs, a, lane);
+    }
     amax = finite_max(x);
   }
   amax = warp_max(amax);
@@ -231,32 +242,48 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
   return lo;
 }
 
-// NP: passes of the block's threads over a page's rows (page * d / 16 / 256).
-template <typename T, int NP>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a, int items,
-                                                             int qrows_per_block) {
+// Query rows of a call with offsets: a block takes `tokens` tokens' heads. Each
+// thread has one row under way, and many blocks on an SM hide the latency (two
+// rows a thread at fewer blocks an SM: 70 us for a call of 8192 tokens with 64
+// heads, against 64).
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads, 5) q8_append_query_kernel(Q8AppendArgs a, int tokens) {
+  ptx::grid_dep_launch();  // (the pages' kernel needs nothing from here)
+  const int tpr = a.d / 16, rpp = kThreads / tpr, j = threadIdx.x % tpr;
+  const int t0 = blockIdx.x * tokens;
+  const int rows = min(tokens, a.N - t0) * a.Hq;
+  int token = -1, at = -1;  // of the row before: a token's heads share them
+  for (int r = threadIdx.x / tpr; r < rows; r += rpp) {
+    const int t = t0 + (tokens == 1 ? 0 : (int)((uint32_t)r / (uint32_t)a.Hq));
+    if (t != token) {
+      token = t;
+      at = -1;
+      const int b = sequence_of(a.cu, a.B, t);
+      int f, n;
+      if (q8::token_range(a.cu, b, a.N, f, n) && t >= f && t < f + n) {
+        const int pos = a.pos[b];
+        if (place_ok(a, pos, n)) at = pos + t - f;
+      }
+    }
+    if (at >= 0) turn_query<T, HALF>(a, (long)t0 * a.Hq + r, at, j);
+  }
+}
+
+// K and V of a call with offsets: a block per (page of a sequence's new tokens,
+// KV head, K or V). NP: passes of the block's threads over a page's rows.
+template <typename T, bool HALF, int NP>
+__global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tpr = a.d / 16, rpp = kThreads / tpr;
   const int j = tid % tpr;
   const long parts = 2l * a.Hkv;
-  if (blockIdx.x >= items * parts) {
-    // query rows
-    const long first = (blockIdx.x - items * parts) * qrows_per_block;
-    for (int r = tid / tpr; r < qrows_per_block; r += rpp) {
-      const long row = first + r;
-      const int t = (int)(row / a.Hq);
-      if (t >= a.N) return;
-      const int b = sequence_of(a.cu, a.B, t);
-      int f, n;
-      if (!q8::token_range(a.cu, b, a.N, f, n) || t < f || t >= f + n) continue;
-      const int pos = a.pos[b];
-      if (place_ok(a, pos, n)) turn_query<T>(a, row, pos + t - f, j);
-    }
-    return;
-  }
-  __shared__ int s_seq, s_page, s_sum[kThreads / 32];
+  __shared__ int s_seq, s_page, s_first, s_n, s_pos, s_sum[kThreads / 32];
   __shared__ float s_max[kThreads / 32];
   const int item = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
+  // (a query kernel before this one is not read from, but ends before this one does)
+  struct Wait {
+    __device__ ~Wait() { ptx::grid_dep_wait(); }
+  } wait;
   const int isv = part & 1, h = part >> 1;
   // item -> (sequence, page of its new tokens): sequences take
   // (pos + n - 1) / page - pos / page + 1 items each, in order
@@ -293,6 +320,9 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a, int
     if (item >= start && item < start + mine) {
       s_seq = b;
       s_page = pos / a.page + item - start;
+      s_first = f;
+      s_n = n;
+      s_pos = pos;
     }
     base += all;
     __syncthreads();
@@ -301,13 +331,37 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a, int
   }
   const int b = s_seq;
   if (b < 0) return;  // more blocks than items
-  int f, n;
-  q8::token_range(a.cu, b, a.N, f, n);
-  const int pos = a.pos[b];
-  const int x0 = max(pos, s_page * a.page);                       // positions of this page's
-  const int x1 = min(pos + n, (int)min((long)(s_page + 1) * a.page, (long)a.T));  // new tokens
+  const int f = s_first, pos = s_pos;
+  const int x0 = max(pos, s_page * a.page);  // positions of this page's new tokens
+  const int x1 = min(pos + s_n, (int)min((long)(s_page + 1) * a.page, (long)a.T));
   const int slot = x0 - s_page * a.page, rows = x1 - x0;
   const int pid = a.table[(long)b * a.max_pages + s_page];
+  int pa, pb;
+  pieces(j, a.rot, pa, pb);
+  const T* src = static_cast<const T*>(isv ? a.v_new : a.k_new);
+  const long row0 = ((long)f + (x0 - pos)) * a.Hkv + h;  // its rows are Hkv apart
+  // rows stay as they were read; each of the two passes over them rotates anew
+  typename Vec8<T>::Raw raw[NP][2];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int r = k * rpp + tid / tpr;
+    if (r < rows) {
+      const T* p = src + (row0 + (long)r * a.Hkv) * a.d;
+      raw[k][0] = Vec8<T>::load_raw(p + pa);
+      raw[k][1] = Vec8<T>::load_raw(p + pb);
+    }
+  }
+  auto row_values = [&](int k, int r, float (&x)[16]) {
+    Vec8<T>::unpack(raw[k][0], x);
+    Vec8<T>::unpack(raw[k][1], x + 8);
+    if (!isv) {
+      float cs[16];
+      turn_of<HALF>(cs, a, x0 + r, j);
+      rotate<HALF>(x, cs, a, j);
+    }
+    return finite_max(x);
+  };
   if (pid < 0 || pid >= a.num_pages) {
     if (tid == 0) atomicOr(a.err, kErrPage);
     return;
@@ -316,28 +370,11 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a, int
   float* sp = (isv ? a.v_scale : a.k_scale) + ph;
   uint8_t* page = (isv ? a.v_pages : a.k_pages) + ph * a.page * a.d;
   const float old = *sp;
-  int pa, pb;
-  pieces(j, a.rot, pa, pb);
-  const T* src = static_cast<const T*>(isv ? a.v_new : a.k_new);
-  const long row0 = ((long)f + (x0 - pos)) * a.Hkv + h;  // its rows are Hkv apart
-  float x[NP][16];
-  float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int r = k * rpp + tid / tpr;
-    if (r < rows) {
-      const T* p = src + (row0 + (long)r * a.Hkv) * a.d;
-      Vec8<T>::load(p + pa, x[k]);
-      Vec8<T>::load(p + pb, x[k] + 8);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int r = k * rpp + tid / tpr;
-    if (r < rows) {
-      if (!isv) rotate(x[k], a.rope + (long)(x0 + r) * a.rot, a.rot, a.style, j);
-      amax = fmaxf(amax, finite_max(x[k]));
-    }
+    float x[16];
+    if (r < rows) amax = fmaxf(amax, row_values(k, r, x));
   }
   amax = warp_max(amax);
   if (lane == 0) s_max[warp] = amax;
@@ -355,42 +392,56 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a, int
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int r = k * rpp + tid / tpr;
-    if (r < rows)
-      put_codes<T>(x[k], s, inv, page + (slot + r) * a.d,
+    float x[16];
+    if (r < rows) {
+      row_values(k, r, x);
+      put_codes<T>(x, s, inv, page + (slot + r) * a.d,
                    held ? held + (row0 + (long)r * a.Hkv) * a.d : nullptr, pa, pb);
+    }
   }
 }
 
-template <typename T>
+template <typename T, bool HALF>
 cudaError_t launch(const Q8AppendArgs& a, cudaStream_t stream) {
   const int tpr = a.d / 16;
-  TraceScope trace("append_q8", stream);
   if (!a.cu) {
+    TraceScope trace("append_q8", stream);
     long warps = (long)a.B * a.Hkv * 2;
     if (a.q) warps += ((long)a.B * a.Hq + 32 / tpr - 1) / (32 / tpr);
     const long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    q8_append_step_kernel<T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    q8_append_step_kernel<T, HALF><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
+  }
+  if (a.q) {
+    // two rounds of a block's rows, or one token's heads
+    const int tokens = std::max(1, 2 * (kThreads / tpr) / a.Hq);
+    const int blocks = (a.N + tokens - 1) / tokens;
+    TraceScope trace("append_q8_query", stream);
+    q8_append_query_kernel<T, HALF><<<blocks, kThreads, 0, stream>>>(a, tokens);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
   // a sequence's n tokens lie on at most n / page + 2 pages
   const long items = (long)a.N / a.page + 2l * (a.B < a.N ? a.B : a.N);
-  const int qrows = 4 * (kThreads / tpr);
-  const long qblocks = a.q ? ((long)a.N * a.Hq + qrows - 1) / qrows : 0;
-  const unsigned blocks = (unsigned)(items * a.Hkv * 2 + qblocks);
-  const int passes = a.page * a.d / 16 / kThreads;
-  if (passes <= 1)
-    q8_append_kernel<T, 1><<<blocks, kThreads, 0, stream>>>(a, (int)items, qrows);
-  else if (passes == 2)
-    q8_append_kernel<T, 2><<<blocks, kThreads, 0, stream>>>(a, (int)items, qrows);
-  else
-    q8_append_kernel<T, 4><<<blocks, kThreads, 0, stream>>>(a, (int)items, qrows);
+  const int passes = a.page * a.d / 16 / kThreads;  // of the threads over a page's rows
+  auto kern = passes <= 1   ? q8_append_kernel<T, HALF, 1>
+              : passes == 2 ? q8_append_kernel<T, HALF, 2>
+                            : q8_append_kernel<T, HALF, 4>;
+  TraceScope trace("append_q8", stream);
+  if (a.q)
+    return q8::launch_pdl(kern, dim3((unsigned)(items * a.Hkv * 2)), dim3(kThreads), 0, stream, a);
+  kern<<<(unsigned)(items * a.Hkv * 2), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_q8_append(const Q8AppendArgs& a, nsa_dtype dtype, cudaStream_t stream) {
-  return dtype == NSA_DTYPE_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+  if (a.style == NSA_ROPE_HALF)
+    return dtype == NSA_DTYPE_BF16 ? launch<__nv_bfloat16, true>(a, stream)
+                                   : launch<float, true>(a, stream);
+  return dtype == NSA_DTYPE_BF16 ? launch<__nv_bfloat16, false>(a, stream)
+                                 : launch<float, false>(a, stream);
 }
 
 }  // namespace nsa

@@ -81,6 +81,14 @@ __device__ __forceinline__ float2 unpack_half(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// Four e4m3 codes as two pairs of halves.
+__device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -195,9 +203,9 @@ struct Feeder {
   // The pages of the chunk at the place.
   __device__ __forceinline__ void look(const Q8AttendArgs& a, ChunkMeta<PP>* meta, int lane) {
     const int ch = at.c + (a.keys == q8::KEYS_BLOCKS ? 0 : u.lo / CK);
-    const long key0 = (long)ch * CK;
-    const int e = (int)(key0 / a.page);
-    coff = PP == 1 ? (int)(key0 % a.page) : 0;
+    const int shift = __ffs(a.page) - 1;  // (a call has fewer than 2^30 tokens or listed keys)
+    const int e = (ch * CK) >> shift;
+    coff = PP == 1 ? ch * CK & (a.page - 1) : 0;
     if (e + PP > gbase + 32 || e < gbase) pages(a, e, lane);
     constexpr int w = CK / PP;
     // rows of the tile see from the first token's window to the last token's
@@ -335,6 +343,8 @@ struct Rows {
       hi[i] = real && u.hi > 0 ? pos + 1 : 0;
       lo[i] = a.keys == q8::KEYS_WINDOW ? max(0, pos + 1 - a.window) : 0;
       float x[D / 4];
+      uint32_t m2 = 0;  // largest magnitudes of the even and odd components (bf16)
+      float big = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32 * PARTS; ++c) {
         const uint4 v = raw.x[i][c];
@@ -346,13 +356,17 @@ struct Rows {
           } else {
             x[(8 * c + 2 * k) % (D / 4)] = __uint_as_float(w[k] << 16);
             x[(8 * c + 2 * k + 1) % (D / 4)] = __uint_as_float(w[k] & 0xffff0000u);
+            m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);  // (order of bits: order of magnitudes)
           }
         }
       }
-      float big = 0.f;
+      if (PARTS == 1 && __vmaxu2(m2, 0x7f7f7f7fu) == 0x7f7f7f7fu) {  // all finite
+        big = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+      } else {
 #pragma unroll
-      for (int j = 0; j < D / 4; ++j)
-        if (fabsf(x[j]) < INFINITY) big = fmaxf(big, fabsf(x[j]));
+        for (int j = 0; j < D / 4; ++j)
+          if (fabsf(x[j]) < INFINITY) big = fmaxf(big, fabsf(x[j]));
+      }
       big = quad_max(big);
       // 2^up brings the largest component to [2^14, 2^15)
       int up = big > 0.f ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
@@ -391,8 +405,8 @@ struct Rows {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t b0 = q8::e4m3x2_to_half2((uint16_t)(w[j] & 0xffffu));
-          const uint32_t b1 = q8::e4m3x2_to_half2((uint16_t)(w[j] >> 16));
+          uint32_t b0, b1;
+          e4m3x4_to_half2x2(w[j], b0, b1);
           mma_f16(z[nt], q[0][4 * half + j], b0, b1);
           if (PARTS == 2) mma_f16(low, q[PARTS - 1][4 * half + j], b0, b1);
         }
@@ -508,8 +522,7 @@ struct Rows {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t x = __byte_perm(w[2 * h], w[2 * h + 1], sel);
-        b[2 * y][h] = q8::e4m3x2_to_half2((uint16_t)(x & 0xffffu));
-        b[2 * y + 1][h] = q8::e4m3x2_to_half2((uint16_t)(x >> 16));
+        e4m3x4_to_half2x2(x, b[2 * y][h], b[2 * y + 1][h]);
       }
     }
   }
@@ -793,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
   if (tid == 0) mm[cta].unit = -1;
   if (cta >= C || V == 0) return;
-  const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
+  const long X0 = q8::split(V, cta, C), X1 = q8::split(V, cta + 1, C);
   const long x0 = X0 + (X1 - X0) * warp / kWarps, x1 = X0 + (X1 - X0) * (warp + 1) / kWarps;
 
   if (x1 > x0) {

@@ -75,13 +75,18 @@ __device__ __forceinline__ int chunks_of(const Q8AttendArgs& a, const Seq& s, in
   return (hi + chunk - 1) / chunk - lo / chunk;
 }
 
+// V c / C, in 32 bits where that holds it (a 64-bit division is slow).
+__device__ __forceinline__ long split(long V, int c, int C) {
+  if (V <= 0xffffffu && C <= 255) return (uint32_t)V * (uint32_t)c / (uint32_t)C;
+  return V * c / C;
+}
+
 // Block that holds position x of V positions split over C blocks: the largest
 // c with V c / C <= x.
 __device__ __forceinline__ int block_of(long x, long V, int C) {
-  int c = (int)((x * C + C - 1) / V);
-  if (c > C - 1) c = C - 1;
-  while (c > 0 && V * c / C > x) --c;
-  while (c < C - 1 && V * (c + 1) / C <= x) ++c;
+  int c = min(C - 1, (int)((float)x * (float)C / (float)V));
+  while (c > 0 && split(V, c, C) > x) --c;
+  while (c < C - 1 && split(V, c + 1, C) <= x) ++c;
   return c;
 }
 

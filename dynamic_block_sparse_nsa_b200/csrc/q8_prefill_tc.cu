@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) reinterpret_cast<q8::MergeMeta*>(a.meta)[cta].unit = -1;
   __syncthreads();
   if (cta < C && V > 0) {
-    const long X0 = V * cta / C, X1 = V * (cta + 1) / C;
+    const long X0 = q8::split(V, cta, C), X1 = q8::split(V, cta + 1, C);
     const int shift = __ffs(a.page) - 1;
     if (warp < 8) {
       Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane,
