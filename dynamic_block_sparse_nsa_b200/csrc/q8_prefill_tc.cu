@@ -13,12 +13,16 @@
 //                    more than 2^5, the epilogue;
 //   warps 8-11       codes to fp16 K and V tiles in shared memory (128-byte
 //                    swizzle), a ring of three;
-//   warp 12          issues the MMAs: while one half's softmax runs, the other
-//                    half's products do;
-//   warp 13          copies the pages' codes to shared memory (a head's page is
-//                    contiguous: one bulk copy each), three tiles ahead.
-// The bound is the softmax: an exponential for every score (16 a clock and SM)
-// takes as long as the two products of it.
+//   warp 12          copies the pages' codes to shared memory (a head's page is
+//                    contiguous: one bulk copy each), three tiles ahead;
+//   warp 13          issues the MMAs: while one half's softmax runs, the other
+//                    half's products do.
+// A half's chain of softmax (an exponential for every score, 16 a clock and SM,
+// is as long as its two products) and products bounds it. 2048 queries of 64
+// heads over 16384 keys (4 KV heads): 1.04 ms, 990 TFLOP/s. What was measured
+// slower: steps of 64 keys with two S tiles a half (the products' overhead
+// doubles: 1.15 ms), 192 registers for the softmax by setmaxnreg (the other
+// roles spill: 1.43 ms), MMAs issued under `lane == 0` (1.19 ms).
 #include <cuda.h>
 
 #include <algorithm>
@@ -106,6 +110,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// One lane of a converged warp: the MMAs and commits are its, the control flow
+// around them the whole warp's (their operands then stay uniform).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -353,7 +365,7 @@ struct Converter {
   }
 };
 
-// ---- MMAs (one thread) ----------------------------------------------------------
+// ---- MMAs (one warp) ----------------------------------------------------------
 
 __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long X1, Smem& sm) {
   Bars& B = sm.bars;
@@ -377,11 +389,14 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
     };
     auto qk = [&](int t, int k) {
       const uint64_t qt = dq + ((t * TILE) >> 4), kt = dk + (((k % kRing) * TILE) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        tc::mma_ss(tmem + s_col(t), k_step(qt, ks), k_step(kt, ks), iqk, ks > 0);
-      if (t == halves - 1) tc::commit(&B.empty[k % kRing]);
-      tc::commit(&B.s_full[t]);
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_ss(tmem + s_col(t), k_step(qt, ks), k_step(kt, ks), iqk, ks > 0);
+        tc::commit(&B.s_full[t]);
+        if (t == halves - 1) tc::commit(&B.empty[k % kRing]);
+      }
+      __syncwarp();
     };
     for (int t = 0; t < halves; ++t) ok = ok && wait(&B.q_full[t], segs[t]++, abort, a.err);
     ok = ok && ready(n);
@@ -396,20 +411,20 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
         if (!ok) break;
         tc::fence_after_sync();
         const uint64_t vt = dv + ((((n + 1) % kRing) * TILE) >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mn_step(vt, ks), ipv,
-                     (i > 0 || ks > 0));
-        if (t == halves - 1) tc::commit(&B.empty[(n + 1) % kRing]);
-        if (!more) {
-          tc::commit(&B.o_full[t]);
-        } else {
-          qk(t, n + 2);
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mn_step(vt, ks), ipv,
+                       (i > 0 || ks > 0));
+          if (t == halves - 1) tc::commit(&B.empty[(n + 1) % kRing]);
+          if (!more) tc::commit(&B.o_full[t]);
         }
+        __syncwarp();
+        if (more) qk(t, n + 2);
       }
     }
   }
-  tc::commit(&B.fin);
+  if (elect_one()) tc::commit(&B.fin);
   if (!ptx::mbar_wait(&B.fin, 0, kWaitNs)) atomicOr(a.err, kErrTimeout);
 }
 
@@ -771,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
   }
   for (int k = tid; k < kNanSlots * D * 8; k += kThreads) (&sm.nan_rows[0][0][0])[k] = 0;
-  if (warp == 12) {
+  if (warp == 13) {
     tc::tmem_alloc(&B.tmem, 512);
     tc::tmem_relinquish();
   }
@@ -796,16 +811,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.run(pl, X0, X1, cta, V, C);
     } else if (warp < 12) {
       Converter{a, warp - 8, lane, shift}.run(pl, X0, X1, sm);
-    } else if (warp == 13) {
+    } else if (warp == 12) {
       copy_pages(a, pl, X0, X1, sm, shift, lane);
-    } else if (lane == 0) {
+    } else {
       issue_mmas(a, pl, X0, X1, sm);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 12) tc::tmem_dealloc(B.tmem, 512);
+  if (warp == 13) tc::tmem_dealloc(B.tmem, 512);
 }
 
 // Joins the partials of a unit that lies in several blocks (see q8_attend.cuh):
