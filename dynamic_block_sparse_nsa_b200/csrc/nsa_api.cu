@@ -156,6 +156,8 @@ nsa_status check_q8(const nsa_params* p) {
     return fail(NSA_ERR_UNSUPPORTED, "pages have 16, 32, 64 or 128 tokens (got sel_block %d)",
                 p->sel_block);
   if (p->T > (1 << 30)) return fail(NSA_ERR_UNSUPPORTED, "T must be <= 2^30");
+  if ((long)p->T * p->Hkv > (1l << 36))
+    return fail(NSA_ERR_UNSUPPORTED, "T * Hkv must be <= 2^36");
   if (p->window < 1 || p->top_n < 1)
     return fail(NSA_ERR_INVALID_ARGUMENT, "window and top_n must be >= 1");
   if (p->top_n > 1024) return fail(NSA_ERR_UNSUPPORTED, "top_n must be <= 1024");

@@ -219,6 +219,23 @@ def test_append_token_by_token_equals_one_call():
     assert torch.equal(one.k_scale, steps.k_scale)
 
 
+def test_append_many_sequences():
+    """More sequences than a block's threads, many without new tokens."""
+    B = 700
+    g = gen(13)
+    past = torch.randint(0, 70, (B,), generator=g).tolist()
+    new = (torch.randint(0, 40, (B,), generator=g) * (torch.rand(B, generator=g) < 0.3)).tolist()
+    p = nsa.params(B, 128, 2, 1, 64, sel_block=32, dtype=BF16)
+    cache = random_cache(p, [a + n for a, n in zip(past, new)], 14)
+    for sc in (cache.k_scale, cache.v_scale):
+        sc.copy_(torch.exp2(torch.floor(torch.log2(sc))))
+    N = sum(new)
+    k, v = (torch.randn(N, 1, 64, generator=g).to(BF16).cuda() for _ in range(2))
+    q = torch.randn(N, 2, 64, generator=g).to(BF16).cuda()
+    cu = i32([0] + torch.tensor(new).cumsum(0).tolist())
+    check_append(p, cache, k, v, i32(past), cu, nsa.rope_table(128, 64), "half", q)
+
+
 def test_append_padded_rows_and_other_pages_stay():
     """Rows behind the last sequence are ignored; pages of no new token keep
     their bytes; q_out may be q."""
@@ -315,6 +332,47 @@ def test_decode_many_sequences_and_long_ones():
         check_attention(got, p, q, cache, i32(lens))
 
 
+def test_decode_far_positions():
+    """The window of a long sequence: pages before it are never looked up."""
+    L = 300001
+    p = nsa.params(1, L + 63, 16, 2, 64, sel_block=64, dtype=F32, window=150)
+    small = random_cache(nsa.params(1, 256, 16, 2, 64, sel_block=64, dtype=F32), [256], 33, extra=0)
+    table = torch.full((1, -(-p.T // 64)), -1, dtype=torch.int32)
+    first = (L - 150) // 64
+    table[0, first:first + 4] = small.page_table[0].cpu()
+    cache = nsa.Q8Cache(small.k_pages, small.v_pages, small.k_scale, small.v_scale, table.cuda())
+    q = torch.randn(1, 16, 64, generator=gen(34)).cuda()
+    got = nsa.nsa_decode_q8(p, q, cache, i32([L]), keys="window")
+    nsa.nsa_check()
+    check_attention(got, p, q, cache, i32([L]), keys="window")
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Pages whose bytes lie past 2^31 of the pool: appended and attended to."""
+    Hkv, page, d = 4, 64, 128
+    P = (1 << 31) // (Hkv * page * d) + 40
+    for new, dt in ((130, BF16), (1, F32)):
+        p = nsa.params(1, 192, 16, Hkv, d, sel_block=page, dtype=dt)
+        table = i32([[P - 1, P - 9, P - 4]])
+        pools = [torch.empty(P, Hkv, page, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        pools = [x.view(torch.float8_e4m3fn) for x in pools]
+        sc = [torch.ones(P, Hkv, device="cuda") for _ in range(2)]
+        cache = nsa.Q8Cache(*pools, *sc, table)
+        k = torch.randn(new, Hkv, d, generator=gen(35)).to(dt).cuda()
+        q = torch.randn(new, 16, d, generator=gen(36)).to(dt).cuda()
+        cu = i32([0, new])
+        nsa.nsa_append_q8(p, k, k, i32([0]), cache, cu_new=cu if new > 1 else None)
+        lens = i32([new])
+        near = nsa.Q8Cache(*[x.view(torch.uint8)[P - 16:].clone().view(torch.float8_e4m3fn) for x in pools],
+                           *[x[P - 16:].clone() for x in sc], table - (P - 16))
+        check_attention(nsa.nsa_prefill_q8(p, q, cache, lens, cu), p, q, near, lens, cu.cpu())
+        last = q[-1:].contiguous()
+        check_attention(nsa.nsa_decode_q8(p, last, cache, lens), p, last, near, lens)
+        nsa.nsa_check()
+        del cache, near, pools
+        torch.cuda.empty_cache()
+
+
 def test_decode_scales_far_apart():
     """Pages whose value scales differ by up to 2^200, with the large ones hardly
     attended: their products leave fp16's and fp32's ranges on the way."""
@@ -331,6 +389,19 @@ def test_decode_scales_far_apart():
         got = nsa.nsa_decode_q8(p, q, cache, i32([256]))
         nsa.nsa_check()
         check_attention(got, p, q, cache, i32([256]))
+
+
+@pytest.mark.parametrize("dt", (BF16, F32))
+def test_negative_softmax_scale(dt):
+    p = nsa.params(1, 200, 16, 1, 128, sel_block=64, dtype=dt, softmax_scale=-0.125)
+    cache = random_cache(p, [200], 37)
+    q = torch.randn(20, 16, 128, generator=gen(38)).to(dt).cuda()
+    lens, cu = i32([200]), i32([0, 20])
+    check_attention(nsa.nsa_prefill_q8(p, q, cache, lens, cu), p, q, cache, lens, cu.cpu(),
+                    scale=-0.125)
+    last = q[-1:].contiguous()
+    check_attention(nsa.nsa_decode_q8(p, last, cache, lens), p, last, cache, lens, scale=-0.125)
+    nsa.nsa_check()
 
 
 def test_decode_softmax_scale_and_extreme_scores():
@@ -440,6 +511,41 @@ def test_prefill_matches_the_definition(case, keys):
         nsa.nsa_check()
         assert (out[-3:] == 5.0).all() and (lse[-3:] == 5.0).all()
         check_attention((out, lse), p, q, cache, i32(lens), cu.cpu(), keys)
+
+
+@pytest.mark.parametrize("Hq,Hkv,lens,new", (
+    (16, 1, [9000], [4]),                      # one unit over every block
+    (16, 2, [70] * 200, [2] * 200),            # many units of one chunk
+    (8, 1, [60, 1] * 600, [9, 1] * 600),       # more sequences than the plan's threads
+    (300, 1, [140, 40], [3, 5]),               # a token's heads fill a tile
+    (3, 1, [700, 259, 5], [700, 131, 5]),      # tokens that straddle tiles
+))
+def test_prefill_many_and_long(Hq, Hkv, lens, new):
+    p = nsa.params(len(lens), max(lens) + 3, Hq, Hkv, 128, sel_block=64)
+    cache = random_cache(p, lens, 47)
+    N = sum(new)
+    q = torch.randn(N, Hq, 128, generator=gen(48)).to(BF16).cuda()
+    cu = i32([0] + torch.tensor(new).cumsum(0).tolist())
+    got = nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu)
+    nsa.nsa_check()
+    check_attention(got, p, q, cache, i32(lens), cu.cpu())
+    again = nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_prefill_scales_far_apart():
+    """Value scales that differ by 2^150 between a tile's pages (tensor memory)."""
+    p = nsa.params(1, 256, 16, 1, 128, sel_block=32)
+    for order in (list(range(8)), list(range(7, -1, -1))):
+        cache = random_cache(p, [256], 49, extra=0)
+        s = torch.exp2(torch.tensor([0.0, 20.0, -100.0, 3.0, 50.0, -126.0, -50.0, 1.0]))[:, None]
+        cache.v_scale.copy_(s)
+        cache.page_table.copy_(i32([order]))
+        q = torch.randn(40, 16, 128, generator=gen(50)).to(BF16).cuda()
+        cu = i32([0, 40])
+        got = nsa.nsa_prefill_q8(p, q, cache, i32([256]), cu)
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, i32([256]), cu.cpu())
 
 
 def test_prefill_rows_equal_single_tokens():
