@@ -179,15 +179,16 @@ struct Feeder {
       if (blk >= 0 && (same & ((1u << lane) - 1))) blk = -1;
       for (int k = 0; k < e; ++k)
         if (list[k] == blk) blk = -1;
-    } else if ((long)i * a.page < u.hi) {
-      blk = i;
+    } else if ((long)i * a.page < u.hi && (long)(i + 1) * a.page > u.lo) {
+      blk = i;  // (a page before the window may be gone)
     }
     pid = blk >= 0 ? a.table[(long)u.b * a.max_pages + blk] : -1;
     if (blk >= 0 && (pid < 0 || pid >= a.num_pages)) {
       atomicOr(a.err, kErrPage);
       pid = blk = -1;
     }
-    ks = vs = 0.f;
+    ks = 0.f;
+    vs = 1.f;
     if (pid >= 0) {
       ks = a.k_scale[(long)pid * a.Hkv + at.h];
       vs = a.v_scale[(long)pid * a.Hkv + at.h];

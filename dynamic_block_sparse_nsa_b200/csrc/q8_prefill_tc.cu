@@ -198,12 +198,12 @@ struct Walk {
   __device__ __forceinline__ bool ends() const { return first + n == at.nc - kQ8TcUnit; }
 };
 
-// Lane j's page of the chunk that begins at key0 (j < 128 / page); -1: none,
-// INT_MAX: not a page number.
+// Lane j's page of the chunk that begins at key0 (j < 128 / page); -1: none
+// (pages before the window may be gone), INT_MAX: not a page number.
 __device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int key0, int lane,
                                        int shift) {
   const int first = key0 + (lane << shift);
-  if (lane >= CK >> shift || first >= u.hi) return -1;
+  if (lane >= CK >> shift || first >= u.hi || first + a.page <= u.lo) return -1;
   const int pid = a.table[(long)u.b * a.max_pages + (first >> shift)];
   return pid < 0 ? INT_MAX : pid;
 }

@@ -289,10 +289,13 @@ NSA_API nsa_status moba_prefill(const nsa_params* p, const void* q, const void* 
  *
  *   k_pages, v_pages  [num_pages, Hkv, sel_block, d] e4m3 bytes, 16-byte
  *              aligned (one head's page is contiguous).
- *   k_scale, v_scale  [num_pages, Hkv] fp32, positive.
+ *   k_scale, v_scale  [num_pages, Hkv] fp32, positive; powers of two where
+ *              nsa_append_q8 continues a page (it writes no others).
  *   page_table [B, ceil(T / sel_block)] int32: token x of sequence b is slot
  *              x % sel_block of page page_table[b, x / sel_block]. Entries of
- *              pages that hold no live token are not used. Sequences may share
+ *              pages without a token that a call reads or writes are not
+ *              used: those behind a sequence's end and, with NSA_KEYS_WINDOW,
+ *              before the first query's window, whose pages may be gone. Sequences may share
  *              pages that none of them appends to.
  * All in device memory. Of nsa_params the calls use B, T (tokens a sequence
  * can have), Hq, Hkv, d, sel_block (16, 32, 64 or 128), dtype (of q, k, v and

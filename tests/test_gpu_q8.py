@@ -560,6 +560,30 @@ def test_prefill_rows_equal_single_tokens():
         torch.testing.assert_close(s[0], lse[i], rtol=2e-5, atol=2e-5)
 
 
+@pytest.mark.parametrize("dt,d,page", ((BF16, 128, 64), (BF16, 128, 32), (F32, 64, 16), (BF16, 64, 128)))
+def test_pages_before_the_window_are_not_looked_up(dt, d, page):
+    lens = torch.tensor([1000, 333, 5], dtype=torch.int32)
+    new = [40, 33, 5]
+    cu = torch.tensor([0, 40, 73, 78], dtype=torch.int32)
+    p = nsa.params(3, 1024, 8, 2, d, dtype=dt, sel_block=page, window=150)
+    cache = random_cache(p, lens.tolist(), 61)
+    table = cache.page_table.cpu()
+    g = gen(62)
+    for count in (1, 2):  # single tokens, then chunks of queries
+        gone = table.clone()
+        for b in range(3):
+            first = int(lens[b]) - (1 if count == 1 else new[b])  # the first query's position
+            gone[b, :max(0, first + 1 - 150) // page] = (-1, 1 << 30)[b % 2]
+        less = nsa.Q8Cache(cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale, gone.cuda())
+        q = torch.randn(3 if count == 1 else 78, 8, d, generator=g).to(dt).cuda()
+        if count == 1:
+            got = nsa.nsa_decode_q8(p, q, less, lens.cuda(), keys="window")
+        else:
+            got = nsa.nsa_prefill_q8(p, q, less, lens.cuda(), cu.cuda(), keys="window")
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, lens, None if count == 1 else cu, "window")
+
+
 @pytest.mark.parametrize("dt,d,Hq", ((BF16, 128, 16), (F32, 64, 4), (BF16, 128, 2)))
 def test_prefill_nan_values_reach_later_queries_only(dt, d, Hq):
     p = nsa.params(1, 200, Hq, 1, d, sel_block=64, dtype=dt, window=30)
