@@ -486,7 +486,7 @@ def _shape(t, name, shape):
 
 def _is(t, name, dtype, device, shape):
     """_dev and _shape in one, as cheap as a decode step wants its checks."""
-    if t is None or (t.dtype is dtype and t.device == device and t.shape == shape
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == device.index
                      and t.is_contiguous()):
         return
     _dev(t, name, dtype, device)
@@ -528,14 +528,15 @@ def nsa_append_q8(p, k_new, v_new, pos, cache, cu_new=None, q=None, rope=None, r
         _is(q_out, "q_out", dt, dev, qs)
     if want_kv and k_out is None:
         k_out = torch.empty_like(k_new)
-    else:
+    elif k_out is not None:
         _is(k_out, "k_out", dt, dev, kv)
     if want_kv and v_out is None:
         v_out = torch.empty_like(k_new)
-    else:
+    elif v_out is not None:
         _is(v_out, "v_out", dt, dev, kv)
     _is(pos, "pos", torch.int32, dev, (p.B,))
-    _is(cu_new, "cu_new", torch.int32, dev, (p.B + 1,))
+    if cu_new is not None:
+        _is(cu_new, "cu_new", torch.int32, dev, (p.B + 1,))
     turn = None
     if rope is not None:
         if rope.dtype is not torch.float32 or rope.device != dev or not rope.is_contiguous():
@@ -564,7 +565,7 @@ def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op):
     else:
         _is(out, "out", dt, dev, shape)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        lse = q.new_empty(shape[:2], dtype=torch.float32)
     else:
         _is(lse, "lse", torch.float32, dev, shape[:2])
     _is(seq_lens, "seq_lens", torch.int32, dev, (p.B,))
