@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t o_col(int t) { return 256u + 128u * t; }
 struct Bars {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t full[kRing], empty[kRing], raw_full[kRaw], raw_empty[kRaw];
-  uint64_t fin;
+  uint64_t fin, marks;
   int abort;
   uint32_t tmem;
   int nan_flag[kNanSlots];
@@ -382,6 +382,8 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
   int n = 0;  // the block's K tile (its V tile is n + 1)
   for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
     const int halves = w.u.rows > 128 ? 2 : 1, chunks = w.n;
+    // (the warp stays together when a wait gives up in some of its lanes)
+    auto all = [&](bool r) { return (bool)__all_sync(0xffffffffu, r); };
     auto ready = [&](int k) {
       const bool r = wait(&B.full[k % kRing], k / kRing, abort, a.err);
       tc::fence_after_sync();
@@ -399,15 +401,15 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
       __syncwarp();
     };
     for (int t = 0; t < halves; ++t) ok = ok && wait(&B.q_full[t], segs[t]++, abort, a.err);
-    ok = ok && ready(n);
+    ok = all(ok && ready(n));
     if (!ok) break;
     for (int t = 0; t < halves; ++t) qk(t, n);
     for (int i = 0; ok && i < chunks; ++i, n += 2) {
       const bool more = i + 1 < chunks;
       // (both are converted ahead; no wait then lies between the products but P's)
-      ok = ready(n + 1) && (!more || ready(n + 2));
-      for (int t = 0; ok && t < halves; ++t) {
-        ok = wait(&B.p_full[t], tiles[t]++, abort, a.err);
+      const bool kv = ready(n + 1) && (!more || ready(n + 2));
+      for (int t = 0; t < halves; ++t) {
+        ok = all(kv && wait(&B.p_full[t], tiles[t]++, abort, a.err));
         if (!ok) break;
         tc::fence_after_sync();
         const uint64_t vt = dv + ((((n + 1) % kRing) * TILE) >> 4);
@@ -546,14 +548,19 @@ struct Softmax {
     return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
   }
 
-  // The unit's NaN marks, if any, are used up (every row's thread sees the same flag).
+  // The unit's NaN marks, if any, are used up: every row's thread sees the same
+  // flag and meets the others before and after they are cleared (two phases of
+  // a barrier of 256, where a unit of one half arrives for both).
   __device__ void use_marks(const Unit& u, int slot) const {
     if (!*(volatile int*)&sm.bars.nan_flag[slot]) return;
     const int threads = u.rows > 128 ? 256 : 128;
-    ptx::named_bar_sync(1, threads);
-    for (int k = 128 * t + row; k < D * 8; k += threads) (&sm.nan_rows[slot][0][0])[k] = 0;
-    if (t == 0 && row == 0) sm.bars.nan_flag[slot] = 0;
-    ptx::named_bar_sync(1, threads);
+    for (int phase = 0; phase < 2; ++phase) {
+      for (int k = threads; k <= 256; k += 128) ptx::mbar_arrive(&sm.bars.marks);
+      wait(&sm.bars.marks, phase, &sm.bars.abort, a.err);
+      if (phase) break;
+      for (int k = 128 * t + row; k < D * 8; k += threads) (&sm.nan_rows[slot][0][0])[k] = 0;
+      if (t == 0 && row == 0) sm.bars.nan_flag[slot] = 0;
+    }
   }
 
   __device__ void run(const Plan& pl, long X0, long X1, int cta, long V, int C) {
@@ -565,7 +572,15 @@ struct Softmax {
     Walk w;
     for (w.start(a, pl, X0, X1); !w.done(); w.next(a, pl)) {
       const Unit& u = w.u;
-      if (t == 1 && u.rows <= 128) continue;
+      // (a unit begins when both halves have ended the one before, so that the
+      // converters, two units ahead at most, never reach a half's marks in use)
+      if (t == 1) {
+        ptx::mbar_arrive(&B.q_full[0]);
+        if (u.rows <= 128) {
+          wait(&B.q_full[0], w.seg, abort, a.err);
+          continue;
+        }
+      }
       load_query(u, w.at.h);
       if (u.rows <= 128 * t + (row & ~31)) {  // no row of the warp is real
         for (int i = 0; i < w.n; ++i) {
@@ -767,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(&B.q_full[t], 128);
+      ptx::mbar_init(&B.q_full[t], t == 0 ? 256 : 128);
       ptx::mbar_init(&B.s_full[t], 1);
       ptx::mbar_init(&B.p_full[t], 128);
       ptx::mbar_init(&B.o_full[t], 1);
@@ -781,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&B.raw_empty[k], 128);
     }
     ptx::mbar_init(&B.fin, 1);
+    ptx::mbar_init(&B.marks, 256);
     B.abort = 0;
     for (int k = 0; k < kNanSlots; ++k) B.nan_flag[k] = 0;
     ptx::fence_mbar_init();
