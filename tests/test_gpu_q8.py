@@ -610,6 +610,31 @@ def test_prefill_nan_values_reach_later_queries_only(dt, d, Hq):
         assert torch.equal(out[clean], base[clean])
 
 
+def test_prefill_nan_values_in_many_short_sequences():
+    """Marks of NaN values in units of one and two tile halves that follow one another."""
+    B, Hq, d = 120, 16, 128
+    new = [(5, 31, 40, 7)[b % 4] for b in range(B)]
+    lens = [50 + 3 * b for b in range(B)]
+    cu = [sum(new[:b]) for b in range(B + 1)]
+    p = nsa.params(B, 512, Hq, 2, d, sel_block=64)
+    cache = random_cache(p, lens, 63)
+    q = torch.randn(cu[-1], Hq, d, generator=gen(64)).bfloat16().cuda()
+    base = nsa.nsa_prefill_q8(p, q, cache, i32(lens), i32(cu))[0]
+    want = torch.zeros(cu[-1], Hq, d, dtype=torch.bool)
+    table, codes = cache.page_table.cpu(), cache.v_pages.view(torch.uint8)
+    for b in range(B):
+        for h in range(2):
+            pos, dim = lens[b] - 1 - (b + h) % new[b], (7 * b + h) % d
+            codes[int(table[b, pos // 64]), h, pos % 64, dim] = 0x7f
+            first = cu[b] + pos - (lens[b] - new[b])
+            want[first:cu[b + 1], 8 * h:8 * h + 8, dim] = True
+    for _ in range(3):
+        out = nsa.nsa_prefill_q8(p, q, cache, i32(lens), i32(cu))[0]
+        nsa.nsa_check()
+        assert torch.equal(torch.isnan(out).cpu(), want)
+        assert torch.equal(out[~want.cuda()], base[~want.cuda()])
+
+
 # ---- together -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dt", (BF16, F32))
