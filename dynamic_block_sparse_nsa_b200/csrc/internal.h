@@ -202,11 +202,12 @@ struct Q8AttendArgs {
 };
 // Chunks of queries on the tensor memory (q8_prefill_tc.cu): bf16, d = 128,
 // pages of 32 tokens or more. The plan is made by the caller, for tiles of
-// kQ8TcRows rows and chunks of kQ8TcKeys keys, kQ8TcUnit chunks more a unit.
-constexpr int kQ8TcRows = 256, kQ8TcKeys = 128, kQ8TcUnit = 8;
+// kQ8TcRows rows and chunks of kQ8TcKeys keys, kQ8TcUnit places more a unit.
+constexpr int kQ8TcRows = 256, kQ8TcKeys = 128;
+constexpr int kQ8TcUnit = 8;
 bool q8_prefill_tc_shape(const nsa_params& p);
 size_t q8_prefill_tc_part_bytes();
-cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, cudaStream_t stream);
+cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, bool split, cudaStream_t stream);
 size_t q8_attend_ws_bytes(const nsa_params& p, bool ragged);
 cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cudaStream_t stream);
 

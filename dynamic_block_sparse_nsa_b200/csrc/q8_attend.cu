@@ -1100,7 +1100,7 @@ __device__ __forceinline__ I block_scan(I mine, I* sums, I& total) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArgs a, int tile_rows,
-                                                               int chunk, int extra) {
+                                                               int chunk, int extra, bool halves) {
   __shared__ long sums[kPlanThreads / 32];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -1139,8 +1139,9 @@ __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArg
       }
       a.plan_seq[t] = b;
       const Seq s = q8::sequence(a, b);
-      mine = (long)(q8::chunks_of(a, s, (t - a.plan_base[b]) * tile_rows, tile_rows, chunk) + extra) *
-             a.Hkv;
+      const int r0 = (t - a.plan_base[b]) * tile_rows;
+      const int weight = halves ? q8::tc_weight(s.n * a.G - r0) : 1;
+      mine = ((long)q8::chunks_of(a, s, r0, tile_rows, chunk) * weight + extra) * a.Hkv;
     }
     const long at = block_scan(mine, sums, all);
     if (t < tiles) a.plan_pre[t + 1] = base + at + mine;
@@ -1231,6 +1232,8 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
   // fill a good part of its 128-row tiles with; below that most of the tile is
   // padding, and the kernel here reads the same codes once per 16 rows.
   const bool tc = ragged && q8_prefill_tc_shape(p) && (long)a.N * a.G >= 32l * p.B;
+  // (and its two halves share the keys where most sequences have rows for one)
+  const bool split = tc && (long)a.N * a.G <= kQ8TcRows / 2 * (long)p.B;
   if (tc) a.tiles = (int)((long)a.N * a.G / kQ8TcRows + p.B);
   if (ragged || a.tiles > kSmemTiles) {
     a.plan_pre = reinterpret_cast<long*>(w + L.pre);
@@ -1238,10 +1241,11 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
     a.plan_base = reinterpret_cast<int*>(w + L.base);
     TraceScope trace("q8_plan", stream);
     const cudaError_t e = q8::launch_pdl(q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a,
-                                         tc ? kQ8TcRows : ROWS, tc ? kQ8TcKeys : CK, tc ? kQ8TcUnit : 0);
+                                         tc ? kQ8TcRows : ROWS, tc ? kQ8TcKeys : CK,
+                                         tc ? kQ8TcUnit : 0, split);
     if (e != cudaSuccess) return e;
   }
-  if (tc) return launch_q8_prefill_tc(a, stream);
+  if (tc) return launch_q8_prefill_tc(a, split, stream);
   const bool bf16 = p.dtype == NSA_DTYPE_BF16;
   using bf = __nv_bfloat16;
   if (p.d == 128) return bf16 ? launch<bf, 128>(a, stream) : launch<float, 128>(a, stream);

@@ -75,6 +75,10 @@ __device__ __forceinline__ int chunks_of(const Q8AttendArgs& a, const Seq& s, in
   return (hi + chunk - 1) / chunk - lo / chunk;
 }
 
+// Places of the tensor-memory kernel's plan for a chunk of a tile: the halves
+// of its rows that are not empty.
+__device__ __forceinline__ int tc_weight(int rows) { return rows > kQ8TcRows / 2 ? 2 : 1; }
+
 // V c / C, in 32 bits where that holds it (a 64-bit division is slow).
 __device__ __forceinline__ long split(long V, int c, int C) {
   if (V <= 0xffffffu && C <= 255) return (uint32_t)V * (uint32_t)c / (uint32_t)C;

@@ -17,11 +17,16 @@
 //                    contiguous: one bulk copy each), three tiles ahead;
 //   warp 13          issues the MMAs: while one half's softmax runs, the other
 //                    half's products do.
+// Where most sequences have rows for one half only (draft tokens), both halves
+// take the same rows and alternate chunks (SPLIT), and half 0 joins the two sums
+// at the unit's end: 16 sequences of 4 queries over 8191 keys 93 -> 75 us (a
+// chunk 1.33 us instead of 2.4; plan, start and merge are some 30 us of it).
 // A half's chain of softmax (an exponential for every score, 16 a clock and SM,
 // is as long as its two products) and products bounds it. 2048 queries of 64
 // heads over 16384 keys (4 KV heads): 1.04 ms, 990 TFLOP/s. What was measured
 // slower: steps of 64 keys with two S tiles a half (the products' overhead
-// doubles: 1.15 ms), 192 registers for the softmax by setmaxnreg (the other
+// doubles: 1.15 ms), two threads a row (16 softmax warps: 1.05 ms, short units
+// 87 us), 192 registers for the softmax by setmaxnreg (the other
 // roles spill: 1.43 ms), MMAs issued under `lane == 0` (1.19 ms).
 #include <cuda.h>
 
@@ -59,7 +64,7 @@ __device__ __forceinline__ uint32_t o_col(int t) { return 256u + 128u * t; }
 struct Bars {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t full[kRing], empty[kRing], raw_full[kRaw], raw_empty[kRaw];
-  uint64_t fin, marks;
+  uint64_t fin, marks, stats_full;
   int abort;
   uint32_t tmem;
   int nan_flag[kNanSlots];
@@ -71,6 +76,7 @@ struct Smem {
   unsigned char kv[kRing][TILE];
   unsigned char raw[kRaw][CK * D];
   Bars bars;
+  float stats[3][128];                 // of half 1's rows in a unit split over the halves
   uint32_t nan_rows[kNanSlots][D][8];  // per component: the tile's tokens that see a NaN value
 };
 
@@ -156,13 +162,15 @@ struct Unit {
 };
 
 // The block's chunks, unit by unit: `n` chunks of the current unit from its
-// chunk `first` on. The plan counts a unit's own cost (query rows in, output
-// rows out) as kQ8TcUnit chunks ahead of its real ones.
+// chunk `first` on. A chunk is `wt` places of the plan, one for each half that
+// has rows; a unit's own cost (query rows in, output rows out) is kQ8TcUnit
+// places ahead of its chunks. A chunk is the block's that has its first place.
+template <bool SPLIT>
 struct Walk {
   Place at;
   Unit u;
   long x, end;
-  int first, n, seg;
+  int first, n, seg, wt;
   __device__ __forceinline__ void start(const Q8AttendArgs& a, const Plan& pl, long x0, long x1) {
     x = x0;
     end = x1;
@@ -174,8 +182,9 @@ struct Walk {
   __device__ __forceinline__ int span() const { return (int)min((long)(at.nc - at.c), end - x); }
   __device__ __forceinline__ void settle(const Q8AttendArgs& a, const Plan& pl) {
     while (x < end) {
-      first = max(0, at.c - kQ8TcUnit);
-      n = at.c + span() - kQ8TcUnit - first;
+      wt = SPLIT ? q8::tc_weight(u.rows) : 1;
+      first = (max(0, at.c - kQ8TcUnit) + wt - 1) / wt;
+      n = (max(0, at.c + span() - kQ8TcUnit) + wt - 1) / wt - first;
       if (n > 0) return;
       step(a, pl);
     }
@@ -195,7 +204,18 @@ struct Walk {
     settle(a, pl);
   }
   __device__ __forceinline__ int key0(int i) const { return (u.lo / CK + first + i) * CK; }
-  __device__ __forceinline__ bool ends() const { return first + n == at.nc - kQ8TcUnit; }
+  __device__ __forceinline__ bool ends() const { return first + n == (at.nc - kQ8TcUnit) / wt; }
+  // Rows for one half only: the halves take alternate chunks of the same rows.
+  __device__ __forceinline__ bool split() const { return SPLIT && wt == 1 && n > 1; }
+  // Tile j of the 2 n in the order of their use: K and V of chunk c in turn, or
+  // (split) each chunk's V behind the next one's K.
+  __device__ __forceinline__ void tile(int j, int& c, bool& v) const {
+    c = j >> 1;
+    v = j & 1;
+    if (!split() || j == 0 || j == 2 * n - 1) return;
+    c = v ? c + 1 : c - 1;
+    v = !v;
+  }
 };
 
 // Lane j's page of the chunk that begins at key0 (j < 128 / page); -1: none
@@ -210,43 +230,59 @@ __device__ __forceinline__ int page_of(const Q8AttendArgs& a, const Unit& u, int
 
 // ---- pages to shared memory (one warp) -------------------------------------------
 
+template <bool SPLIT>
 __device__ void copy_pages(const Q8AttendArgs& a, const Plan& pl, long X0, long X1, Smem& sm,
                            int shift, int lane) {
   Bars& B = sm.bars;
   volatile int* abort = &B.abort;
   const uint32_t bytes = (uint32_t)D << shift;
-  Walk w;
+  Walk<SPLIT> w;
   bool ok = true;
   int n = 0;  // the block's tile
   for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
-    const int chunks = w.n;
     int key0 = w.key0(0);
     int pid = page_of(a, w.u, key0, lane, shift);  // lane j: page j of the chunk
-    for (int i = 0; ok && i < chunks; ++i) {
-      if (pid >= a.num_pages) {
-        atomicOr(a.err, kErrPage);
-        pid = -1;
-      }
-      const bool mine = pid >= 0;
-      const uint32_t live = __ballot_sync(0xffffffffu, mine);
-      const long from = ((long)pid * a.Hkv + w.at.h) << (shift + 7);
+    // the next chunk's, looked up ahead; a number that is none is left out
+    auto step = [&] {
+      const int now = pid < a.num_pages ? pid : -1;
+      if (now != pid) atomicOr(a.err, kErrPage);
       key0 += CK;
-      pid = page_of(a, w.u, key0, lane, shift);  // the next chunk's, ahead
-      for (int v = 0; ok && v < 2; ++v, ++n) {
-        const int r = n % kRaw;
-        if (n >= kRaw) ok = wait(&B.raw_empty[r], n / kRaw - 1, abort, a.err);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          B.live[r] = live;
-          ptx::mbar_arrive_expect_tx(&B.raw_full[r], __popc(live) * bytes);
-        }
-        __syncwarp();
-        if (mine)
-          ptx::bulk_load(sm.raw[r] + lane * bytes, (v ? a.v_pages : a.k_pages) + from, bytes,
-                         &B.raw_full[r]);
+      pid = page_of(a, w.u, key0, lane, shift);
+      return now;
+    };
+    // one tile: every lane its page
+    auto put = [&](int page, bool v) {
+      const bool mine = page >= 0;
+      const uint32_t live = __ballot_sync(0xffffffffu, mine);
+      const long from = ((long)page * a.Hkv + w.at.h) << (shift + 7);
+      const int r = n % kRaw;
+      if (n >= kRaw) ok = wait(&B.raw_empty[r], n / kRaw - 1, abort, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (lane == 0) {
+        B.live[r] = live;
+        ptx::mbar_arrive_expect_tx(&B.raw_full[r], __popc(live) * bytes);
+      }
+      __syncwarp();
+      if (mine)
+        ptx::bulk_load(sm.raw[r] + lane * bytes, (v ? a.v_pages : a.k_pages) + from, bytes,
+                       &B.raw_full[r]);
+      ++n;
+    };
+    if (w.split()) {
+      int now = step();
+      put(now, false);
+      for (int i = 1; ok && i <= w.n; ++i) {
+        const int before = now;
+        if (i < w.n) put(now = step(), false);
+        if (ok) put(before, true);
+      }
+    } else {
+      for (int i = 0; ok && i < w.n; ++i) {
+        const int now = step();
+        // (one copy of the code: unrolled, the call of 2048 queries takes 3 % longer)
+#pragma unroll 1
+        for (int v = 0; ok && v < 2; ++v) put(now, v);
       }
     }
   }
@@ -323,10 +359,11 @@ struct Converter {
     __threadfence_block();
   }
 
+  template <bool SPLIT>
   __device__ void run(const Plan& pl, long X0, long X1, Smem& sm) const {
     Bars& B = sm.bars;
     volatile int* abort = &B.abort;
-    Walk w;
+    Walk<SPLIT> w;
     int n = 0;  // the block's tile
 #pragma unroll 1
     for (w.start(a, pl, X0, X1); !w.done(); w.next(a, pl)) {
@@ -336,6 +373,12 @@ struct Converter {
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i, ++n) {
         const int r = n % kRaw, buf = n % kRing;
+        bool isv = i & 1;
+        if (SPLIT) {
+          int c;
+          w.tile(i, c, isv);
+          key0 = w.key0(c);
+        }
         wait(&B.raw_full[r], n / kRaw, abort, a.err);
         const uint32_t live = B.live[r];
         uint4 x[8];
@@ -351,7 +394,7 @@ struct Converter {
             if (pos < lo || pos >= hi || !(live >> (row(k) >> shift) & 1u))
               x[k] = make_uint4(0, 0, 0, 0);
           }
-          if (i & 1)
+          if (isv)
             mark_nan(x, w.u.s.len - w.u.s.n + w.u.tok0, w.u.tok1 - w.u.tok0, key0,
                      sm.nan_rows[slot], &B.nan_flag[slot]);
         }
@@ -359,7 +402,7 @@ struct Converter {
         store(x, sm.kv[buf]);
         ptx::fence_proxy_async();
         ptx::mbar_arrive(&B.full[buf]);
-        if (i & 1) key0 += CK;
+        if (!SPLIT && (i & 1)) key0 += CK;
       }
     }
   }
@@ -367,6 +410,7 @@ struct Converter {
 
 // ---- MMAs (one warp) ----------------------------------------------------------
 
+template <bool SPLIT>
 __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long X1, Smem& sm) {
   Bars& B = sm.bars;
   volatile int* abort = &B.abort;
@@ -377,11 +421,13 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
   const uint64_t dk = tc::sdesc(ptx::smem_u32(sm.kv), 16, 1024, tc::kSw128);
   const uint64_t dv = tc::sdesc(ptx::smem_u32(sm.kv), ATOM, 1024, tc::kSw128);
   int segs[2] = {0, 0}, tiles[2] = {0, 0};  // per half: units begun, P tiles taken
-  Walk w;
+  Walk<SPLIT> w;
   bool ok = true;
   int n = 0;  // the block's K tile (its V tile is n + 1)
   for (w.start(a, pl, X0, X1); ok && !w.done(); w.next(a, pl)) {
-    const int halves = w.u.rows > 128 ? 2 : 1, chunks = w.n;
+    const int chunks = w.n;
+    const bool split = w.split();
+    const int halves = w.u.rows > 128 || split ? 2 : 1;
     // (the warp stays together when a wait gives up in some of its lanes)
     auto all = [&](bool r) { return (bool)__all_sync(0xffffffffu, r); };
     auto ready = [&](int k) {
@@ -389,21 +435,48 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
       tc::fence_after_sync();
       return r;
     };
-    auto qk = [&](int t, int k) {
+    auto qk = [&](int t, int k, bool free) {
       const uint64_t qt = dq + ((t * TILE) >> 4), kt = dk + (((k % kRing) * TILE) >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           tc::mma_ss(tmem + s_col(t), k_step(qt, ks), k_step(kt, ks), iqk, ks > 0);
         tc::commit(&B.s_full[t]);
-        if (t == halves - 1) tc::commit(&B.empty[k % kRing]);
+        if (free) tc::commit(&B.empty[k % kRing]);
       }
       __syncwarp();
     };
     for (int t = 0; t < halves; ++t) ok = ok && wait(&B.q_full[t], segs[t]++, abort, a.err);
+    auto pv = [&](int t, int k, bool begun, bool free, bool ends) {
+      const uint64_t vt = dv + (((k % kRing) * TILE) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mn_step(vt, ks), ipv,
+                     (begun || ks > 0));
+        if (free) tc::commit(&B.empty[k % kRing]);
+        if (ends) tc::commit(&B.o_full[t]);
+      }
+      __syncwarp();
+    };
     ok = all(ok && ready(n));
+    if (split) ok = all(ok && ready(n + 1));
     if (!ok) break;
-    for (int t = 0; t < halves; ++t) qk(t, n);
+    for (int t = 0; t < halves; ++t) qk(t, split ? n + t : n, split || t == halves - 1);
+    if (split) {
+      for (int i = 0; i < chunks; ++i) {
+        const int t = i & 1, kv = n + (i < chunks - 1 ? 2 * i + 2 : 2 * i + 1);
+        const bool more = i + 2 < chunks;
+        const bool r = ready(kv) && (!more || ready(kv + 1));
+        ok = all(r && wait(&B.p_full[t], tiles[t]++, abort, a.err));
+        if (!ok) break;
+        tc::fence_after_sync();
+        pv(t, kv, i > 1, true, !more);
+        if (more) qk(t, kv + 1, true);
+      }
+      n += 2 * chunks;
+      continue;
+    }
     for (int i = 0; ok && i < chunks; ++i, n += 2) {
       const bool more = i + 1 < chunks;
       // (both are converted ahead; no wait then lies between the products but P's)
@@ -412,17 +485,8 @@ __device__ void issue_mmas(const Q8AttendArgs& a, const Plan& pl, long X0, long 
         ok = all(kv && wait(&B.p_full[t], tiles[t]++, abort, a.err));
         if (!ok) break;
         tc::fence_after_sync();
-        const uint64_t vt = dv + ((((n + 1) % kRing) * TILE) >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + ks * 8, mn_step(vt, ks), ipv,
-                       (i > 0 || ks > 0));
-          if (t == halves - 1) tc::commit(&B.empty[(n + 1) % kRing]);
-          if (!more) tc::commit(&B.o_full[t]);
-        }
-        __syncwarp();
-        if (more) qk(t, n + 2);
+        pv(t, n + 1, i > 0, t == halves - 1, !more);
+        if (more) qk(t, n + 2, t == halves - 1);
       }
     }
   }
@@ -436,6 +500,7 @@ struct Softmax {
   const Q8AttendArgs& a;
   Smem& sm;
   int t, row;      // half, row of it
+  int r1;          // the half's first row in the unit's
   uint32_t tl;     // the warp's lanes of tensor memory
   int shift;       // log2 of the page
   float qf;        // row factor of the scores
@@ -443,7 +508,7 @@ struct Softmax {
 
   // The row's query, scaled into fp16's range, into the half's tile.
   __device__ __forceinline__ void load_query(const Unit& u, int h) {
-    const int r = u.r0 + 128 * t + row;
+    const int r = u.r0 + r1 + row;
     const bool real = r < u.s.n * a.G;
     const int pos = u.s.len - u.s.n + r / a.G;
     // (rows behind the last see everything: their warps need no masks)
@@ -485,6 +550,7 @@ struct Softmax {
           make_uint4(y[0], y[1], y[2], y[3]);
     }
     ptx::fence_proxy_async();
+    tc::fence_before_sync();  // (the unit before was read from tensor memory)
     ptx::mbar_arrive(&sm.bars.q_full[t]);
   }
 
@@ -563,43 +629,55 @@ struct Softmax {
     }
   }
 
+  template <bool SPLIT>
   __device__ void run(const Plan& pl, long X0, long X1, int cta, long V, int C) {
     Bars& B = sm.bars;
     volatile int* abort = &B.abort;
     const int lane = threadIdx.x & 31;
     q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
     int tiles = 0, units = 0;
-    Walk w;
+    int others = 0, splits = 0;  // half 0: units that half 1 had a part in; split ones
+    Walk<SPLIT> w;
     for (w.start(a, pl, X0, X1); !w.done(); w.next(a, pl)) {
       const Unit& u = w.u;
       // (a unit begins when both halves have ended the one before, so that the
       // converters, two units ahead at most, never reach a half's marks in use)
+      const bool split = w.split();
+      const int step = split ? 2 : 1;
+      r1 = split ? 0 : 128 * t;
       if (t == 1) {
         ptx::mbar_arrive(&B.q_full[0]);
-        if (u.rows <= 128) {
+        if (u.rows <= r1) {
           wait(&B.q_full[0], w.seg, abort, a.err);
           continue;
         }
       }
       load_query(u, w.at.h);
-      if (u.rows <= 128 * t + (row & ~31)) {  // no row of the warp is real
-        for (int i = 0; i < w.n; ++i) {
+      if (u.rows <= r1 + (row & ~31)) {  // no row of the warp is real
+        for (int i = split ? t : 0; i < w.n; i += step) {
           wait(&B.s_full[t], tiles++, abort, a.err);
           ptx::mbar_arrive(&B.p_full[t]);
         }
         wait(&B.o_full[t], units++, abort, a.err);
-        // (it has read the marks' flag like the others)
-        use_marks(u, w.seg % kNanSlots);
+        // (it reads the marks' flag when the others do: all values are in)
+        if (split && t == 0) wait(&B.o_full[1], others, abort, a.err);
+        others += u.rows > 128 || split;
+        splits += split;
+        if (split && t == 1)
+          ptx::mbar_arrive(&B.stats_full);
+        else
+          use_marks(u, w.seg % kNanSlots);
         continue;
       }
       float m = -INFINITY, M = -INFINITY, l = 0.f;
       const int chunks = w.n, h = w.at.h;
-      int key0 = w.key0(0);
+      int key0 = w.key0(split ? t : 0);
+      bool begun = false;
       Pages pg{page_of(a, u, key0, lane, shift), 0.f, 0.f, 0.f};
       pg.scales(a, h);
 #pragma unroll 1
-      for (int i = 0; i < chunks; ++i, key0 += CK) {
-        Pages next{page_of(a, u, key0 + CK, lane, shift), 0.f, 0.f, 0.f};
+      for (int i = split ? t : 0; i < chunks; i += step, key0 += step * CK) {
+        Pages next{page_of(a, u, key0 + step * CK, lane, shift), 0.f, 0.f, 0.f};
         pg.lv = __log2f(pg.vs);
         const bool mine = lane < CK >> shift;
         const bool masked = __any_sync(
@@ -658,7 +736,7 @@ struct Softmax {
         const bool move = ref > M + kLag;
         const float ao = move && M != -INFINITY ? ptx::ex2(M - ref) : 1.f;
         if (move) M = ref;
-        if (i > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
+        if ((SPLIT ? begun : i > 0) && __any_sync(0xffffffffu, ao != 1.f)) {
 #pragma unroll 1
           for (int q4 = 0; q4 < 8; ++q4) {
             uint32_t o[16];
@@ -716,18 +794,44 @@ struct Softmax {
         tc::fence_before_sync();
         ptx::mbar_arrive(&B.p_full[t]);
         pg = next;
+        begun = true;
       }
 
       // ---- epilogue ----
       wait(&B.o_full[t], units++, abort, a.err);
       tc::fence_after_sync();
-      const int r = u.r0 + 128 * t + row;
+      const int r = u.r0 + r1 + row;
       const bool real = r < u.s.n * a.G;
       const bool whole = w.first == 0 && w.ends();
       const float base = m == -INFINITY ? 0.f : m, oref = M == -INFINITY ? 0.f : M;
       // in two factors: 2^(M - m) alone can leave fp32's range
-      const float half = ptx::ex2(0.5f * (oref - base)), f = l == 0.f ? 0.f : half / l;
-      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+      const float half = ptx::ex2(0.5f * (oref - base));
+      float f = l == 0.f ? 0.f : half / l;
+      float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+      float half1 = 0.f, f1 = 0.f;
+      if (split) {
+        // half 1 leaves its sums to half 0, which reads its O too (the next unit
+        // begins behind that)
+        if (t == 1) {
+          sm.stats[0][row] = half;
+          sm.stats[1][row] = f;
+          sm.stats[2][row] = lse2;
+          ptx::mbar_arrive(&B.stats_full);
+          continue;
+        }
+        wait(&B.o_full[1], others, abort, a.err);
+        wait(&B.stats_full, splits++, abort, a.err);
+        tc::fence_after_sync();
+        half1 = sm.stats[0][row];
+        const float lse1 = sm.stats[2][row], top = fmaxf(lse2, lse1);
+        const float b2 = top == -INFINITY ? 0.f : top;
+        const float w0 = ptx::ex2(lse2 - b2), w1 = ptx::ex2(lse1 - b2), sum = w0 + w1;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        f *= w0 * inv;
+        f1 = sm.stats[1][row] * w1 * inv;
+        lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+      }
+      others += u.rows > 128 || split;
       const int slot = w.seg % kNanSlots;
       const bool nan = *(volatile int*)&B.nan_flag[slot] != 0;
       float* part = a.part + (2l * cta + (w.first > 0 ? 0 : 1)) * kPart;
@@ -736,10 +840,15 @@ struct Softmax {
       for (int q4 = 0; q4 < 4; ++q4) {
         uint32_t o[32];
         tc::ld32_sync(tl + o_col(t) + 32 * q4, o);
-        if (!real) continue;
         float y[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * half * f;
+        if (split) {
+          tc::ld32_sync(tl + o_col(1) + 32 * q4, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = fmaf(__uint_as_float(o[e]) * half1, f1, y[e]);
+        }
+        if (!real) continue;
         if (nan) {
           const int tk = r / a.G - u.tok0;
 #pragma unroll
@@ -751,7 +860,7 @@ struct Softmax {
 #pragma unroll
           for (int e = 0; e < 32; e += 16) store32(dst + 32 * q4 + e, &y[e]);
         } else {
-          float4* to = reinterpret_cast<float4*>(part) + 8 * q4 * ROWS + 128 * t + row;
+          float4* to = reinterpret_cast<float4*>(part) + 8 * q4 * ROWS + r1 + row;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             to[e * ROWS] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
@@ -761,7 +870,7 @@ struct Softmax {
         if (whole) {
           if (a.lse) a.lse[out_row(u, w.at.h, r)] = lse2 * q8::kLn2;
         } else {
-          part[(long)ROWS * D + 128 * t + row] = lse2;
+          part[(long)ROWS * D + r1 + row] = lse2;
         }
       }
       if (t == 0 && row == 0 && w.first > 0 && w.ends()) {
@@ -773,6 +882,7 @@ struct Softmax {
   }
 };
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     q8_prefill_tc_kernel(const __grid_constant__ Q8AttendArgs a) {
   extern __shared__ unsigned char raw[];
@@ -797,6 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(&B.fin, 1);
     ptx::mbar_init(&B.marks, 256);
+    ptx::mbar_init(&B.stats_full, 128);
     B.abort = 0;
     for (int k = 0; k < kNanSlots; ++k) B.nan_flag[k] = 0;
     ptx::fence_mbar_init();
@@ -814,7 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Plan pl{a.plan_pre, a.plan_seq, a.plan_base, nullptr, a.plan_base[a.B], 0};
   const long V = pl.tiles ? pl.pre[pl.tiles] : 0;
-  const int C = (int)max(1l, min((long)gridDim.x, V));
+  // (two places a block: one chunk of every unit that goes on in it)
+  const int C = (int)max(1l, min((long)gridDim.x, (SPLIT ? V / 2 : V)));
   const int cta = blockIdx.x;
   if (tid == 0) reinterpret_cast<q8::MergeMeta*>(a.meta)[cta].unit = -1;
   __syncthreads();
@@ -822,15 +934,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long X0 = q8::split(V, cta, C), X1 = q8::split(V, cta + 1, C);
     const int shift = __ffs(a.page) - 1;
     if (warp < 8) {
-      Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane,
+      Softmax s{a, sm, warp >> 2, (warp & 3) * 32 + lane, 0,
                 B.tmem + ((uint32_t)((warp & 3) * 32) << 16), shift, 0.f, 0, 0};
-      s.run(pl, X0, X1, cta, V, C);
+      s.run<SPLIT>(pl, X0, X1, cta, V, C);
     } else if (warp < 12) {
-      Converter{a, warp - 8, lane, shift}.run(pl, X0, X1, sm);
+      Converter{a, warp - 8, lane, shift}.run<SPLIT>(pl, X0, X1, sm);
     } else if (warp == 12) {
-      copy_pages(a, pl, X0, X1, sm, shift, lane);
+      copy_pages<SPLIT>(a, pl, X0, X1, sm, shift, lane);
     } else {
-      issue_mmas(a, pl, X0, X1, sm);
+      issue_mmas<SPLIT>(a, pl, X0, X1, sm);
     }
   }
   tc::fence_before_sync();
@@ -892,13 +1004,14 @@ bool q8_prefill_tc_shape(const nsa_params& p) {
 
 size_t q8_prefill_tc_part_bytes() { return (size_t)kPart * 4 * 2 * kQ8MaxBlocks; }
 
-cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, cudaStream_t stream) {
+cudaError_t launch_q8_prefill_tc(const Q8AttendArgs& a, bool split, cudaStream_t stream) {
   constexpr int smem = sizeof(Smem) + 1024;
   cudaError_t e;
-  if ((e = ensure_dyn_smem((const void*)q8_prefill_tc_kernel, smem)) != cudaSuccess) return e;
+  auto kern = split ? q8_prefill_tc_kernel<true> : q8_prefill_tc_kernel<false>;
+  if ((e = ensure_dyn_smem((const void*)kern, smem)) != cudaSuccess) return e;
   {
     TraceScope trace("q8_prefill_tc", stream);
-    if ((e = q8::launch_pdl(q8_prefill_tc_kernel, dim3(a.blocks), dim3(kThreads), smem, stream, a)) !=
+    if ((e = q8::launch_pdl(kern, dim3(a.blocks), dim3(kThreads), smem, stream, a)) !=
         cudaSuccess)
       return e;
   }
