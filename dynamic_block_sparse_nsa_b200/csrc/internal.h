@@ -199,6 +199,7 @@ struct Q8AttendArgs {
   int* plan_seq;
   int* plan_base;
   int tiles, rt, blocks, min_chunks;
+  int by_unit;             // whole units to a block: 1 as many each, 2 by their chunks
 };
 // Chunks of queries on the tensor memory (q8_prefill_tc.cu): bf16, d = 128,
 // pages of 32 tokens or more. The plan is made by the caller, for tiles of

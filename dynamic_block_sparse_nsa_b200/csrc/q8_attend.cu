@@ -44,6 +44,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int CK = 64;       // keys per chunk
 constexpr int NS = CK / 8;   // score tiles of 8 keys
 constexpr int ROWS = 16;     // query rows per tile
+constexpr int kUnitChunks = 4 * kWarps;  // most chunks of a unit that one block takes whole
 constexpr int SLOTS = 3;     // of a warp's ring
 constexpr int kSmemTiles = 1024;  // tiles whose prefix a block computes itself
 
@@ -802,12 +803,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long V = pl.tiles ? pl.pre[pl.tiles] : 0;
   // few chunks: fewer blocks, so that a block's warps share its merge
   const long want = (V + a.min_chunks - 1) / a.min_chunks;
-  const int C = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
+  const int C = (int)(a.by_unit || want >= gridDim.x ? gridDim.x : want > 0 ? want : 1);
   const int cta = blockIdx.x;
   q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
   if (tid == 0) mm[cta].unit = -1;
   if (cta >= C || V == 0) return;
-  const long X0 = q8::split(V, cta, C), X1 = q8::split(V, cta + 1, C);
+  long X0 = q8::split(V, cta, C), X1 = q8::split(V, cta + 1, C);
+  if (a.by_unit == 1) {
+    const long units = (long)pl.tiles * a.Hkv;
+    X0 = q8::unit_place(pl, a.Hkv, (int)q8::split(units, cta, C));
+    X1 = q8::unit_place(pl, a.Hkv, (int)q8::split(units, cta + 1, C));
+  } else if (a.by_unit == 2) {
+    X0 = q8::unit_start(pl, a.Hkv, X0);
+    X1 = q8::unit_start(pl, a.Hkv, X1);
+  }
   const long x0 = X0 + (X1 - X0) * warp / kWarps, x1 = X0 + (X1 - X0) * (warp + 1) / kWarps;
 
   if (x1 > x0) {
@@ -1160,6 +1169,7 @@ cudaError_t launch(const Q8AttendArgs& a, cudaStream_t stream) {
     if ((e = q8::launch_pdl(kern, dim3(a.blocks), dim3(kThreads), smem, stream, a)) != cudaSuccess)
       return e;
   }
+  if (a.by_unit) return cudaSuccess;
   TraceScope trace("q8_merge", stream);
   return q8::launch_pdl(q8_merge_kernel<T, D>, dim3(a.blocks, D / 32), dim3(32 * kMergeWarps), 0, stream,
                     a);
@@ -1225,6 +1235,22 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
   a.rt = (a.G + ROWS - 1) / ROWS;
   a.blocks = std::min(device_sm_count(), kQ8MaxBlocks);
   a.min_chunks = 8;
+  // Units of few chunks: whole ones to a block, which leaves no partials and
+  // saves the merge kernel (3 to 6 us; a pass of a block's warps over a chunk
+  // each takes 2 us). With the most chunks a unit can have, that may cost 1.25
+  // passes more than an even split does: 4 units of 16 chunks take 14.8 us both
+  // ways, of 22 chunks 17.4 us whole and 14.6 split; 128 units of 22 chunks 19
+  // and 24.5 us, of 32 chunks 22 and 27. Few chunks and as many units as blocks,
+  // or windows and lists, make units alike; else they are dealt by their chunks.
+  const long most = a.keys == q8::KEYS_BLOCKS   ? ((long)a.n * a.page + CK - 1) / CK
+                    : a.keys == q8::KEYS_WINDOW ? ((long)a.window + ROWS + 2 * CK - 2) / CK
+                                                : ((long)a.T + CK - 1) / CK;
+  const long units = (long)a.tiles * a.Hkv, per = (units + a.blocks - 1) / a.blocks;
+  const double even = (double)units * most / (kWarps * (double)a.blocks);
+  a.by_unit = most > kUnitChunks || per * most > kWarps * (std::max(1.0, even) + 1.25) ? 0
+              : a.keys == q8::KEYS_ALL && units > a.blocks                             ? 2
+                                                                                       : 1;
+  if (a.by_unit) a.blocks = (int)std::min<long>(a.blocks, units);
   a.plan_pre = nullptr;
   a.plan_seq = nullptr;
   a.plan_base = nullptr;

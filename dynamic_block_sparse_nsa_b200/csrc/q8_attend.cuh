@@ -134,6 +134,21 @@ struct Place {
   }
 };
 
+// The place that unit u (of tiles x KV heads) begins at.
+__device__ __forceinline__ long unit_place(const Plan& pl, int hkv, int u) {
+  const int tile = u / hkv;
+  if (tile >= pl.tiles) return pl.pre[pl.tiles];
+  return pl.pre[tile] + (u - tile * hkv) * ((pl.pre[tile + 1] - pl.pre[tile]) / hkv);
+}
+
+// The first place at or behind x at which a unit begins.
+__device__ __forceinline__ long unit_start(const Plan& pl, int hkv, long x) {
+  if (x >= pl.pre[pl.tiles]) return x;
+  Place at;
+  at.init(pl, hkv, x);
+  return at.c == 0 ? x : x - at.c + at.nc;
+}
+
 // Per block: the unit of slot 2 c when that unit ends in the block (else -1),
 // and the block it begins in.
 struct MergeMeta {

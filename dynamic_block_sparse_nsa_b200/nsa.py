@@ -539,7 +539,8 @@ def nsa_append_q8(p, k_new, v_new, pos, cache, cu_new=None, q=None, rope=None, r
         _is(cu_new, "cu_new", torch.int32, dev, (p.B + 1,))
     turn = None
     if rope is not None:
-        if rope.dtype is not torch.float32 or rope.device != dev or not rope.is_contiguous():
+        if (rope.dtype is not torch.float32 or rope.get_device() != dev.index
+                or not rope.is_contiguous()):
             _dev(rope, "rope", torch.float32, dev)
         if rope.dim() != 3 or rope.shape[1] != 2:
             raise ValueError(f"rope must be [len, 2, dim / 2], got {list(rope.shape)}")
@@ -565,15 +566,15 @@ def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op):
     else:
         _is(out, "out", dt, dev, shape)
     if lse is None:
-        lse = q.new_empty(shape[:2], dtype=torch.float32)
+        lse = cache.k_scale.new_empty(shape[:2])
     else:
         _is(lse, "lse", torch.float32, dev, shape[:2])
     _is(seq_lens, "seq_lens", torch.int32, dev, (p.B,))
     if ws is None:
         ws = workspace(p, op, dev)
-    elif ws.device != dev or not ws.is_contiguous():
+    elif ws.get_device() != dev.index or not ws.is_contiguous():
         _dev(ws, "ws", None, dev)
-    return out, lse, ws, ws.numel() * ws.element_size()
+    return out, lse, ws, ws.nbytes
 
 
 def nsa_decode_q8(p, q, cache, seq_lens, keys="all", sel_idx=None, out=None, lse=None, ws=None,
@@ -584,7 +585,8 @@ def nsa_decode_q8(p, q, cache, seq_lens, keys="all", sel_idx=None, out=None, lse
     out, lse, ws, nbytes = _attend_q8_args(p, q, p.B, cache, seq_lens, keys, out, lse, ws,
                                            OP_DECODE_Q8)
     dev = cache.device
-    _is(sel_idx, "sel_idx", torch.int32, dev, (p.B, p.Hkv, p.top_n))
+    if sel_idx is not None:
+        _is(sel_idx, "sel_idx", torch.int32, dev, (p.B, p.Hkv, p.top_n))
     _call(LIB.nsa_decode_q8, dev, stream, ctypes.byref(p), cache.ref, _addr(q), _addr(seq_lens),
           KEYS[keys], _addr(sel_idx), _addr(out), _addr(lse), _addr(ws), nbytes)
     return out, lse

@@ -332,6 +332,24 @@ def test_decode_many_sequences_and_long_ones():
         check_attention(got, p, q, cache, i32(lens))
 
 
+@pytest.mark.parametrize("longest", (300, 1400, 2000))
+def test_decode_lengths_far_apart_in_few_chunks(longest):
+    """Whole units to a block, as many each or by their chunks: most lengths are
+    short, empty ones among them, and the long ones lie together."""
+    B = 70
+    lens = [(b * 7) % 9 for b in range(B)]
+    lens[20:24] = [longest, longest - 63, longest // 2, 64]
+    for Hq, Hkv, dt, page in ((12, 3, BF16, 64), (8, 1, F32, 16), (40, 1, BF16, 32)):
+        p = nsa.params(B, longest, Hq, Hkv, 64, dtype=dt, sel_block=page, window=longest - 100)
+        cache = random_cache(p, lens, 71)
+        q = torch.randn(B, Hq, 64, generator=gen(72)).to(dt).cuda()
+        n = torch.tensor(lens, dtype=torch.int32)
+        for keys in ("all", "window"):
+            got = nsa.nsa_decode_q8(p, q, cache, n.cuda(), keys=keys)
+            nsa.nsa_check()
+            check_attention(got, p, q, cache, n, keys=keys)
+
+
 def test_decode_far_positions():
     """The window of a long sequence: pages before it are never looked up."""
     L = 300001
