@@ -14,8 +14,12 @@
 // Bound by bytes (each input read once, each output written once) for long
 // calls and by latency for one token per sequence. A (page, head) of K or V is
 // one block's work: its rows stay in registers between the maximum and the
-// codes, so nothing is read from memory twice; blocks behind those rotate query rows. With
-// one token per sequence a warp takes a (sequence, head) of K or V instead.
+// codes, so nothing is read from memory twice. Query rows have a kernel of their
+// own ahead of it, which the pages' blocks overlap. With one token per sequence a
+// warp takes a (sequence, head) of K or V instead, and more warps the query rows.
+// Measured, 64 query heads on 4 KV heads, d = 128, bf16: 8192 tokens 64 us, 4.9
+// TB/s in and out (loads in flight bound the query rows); 32 sequences of a token
+// each 3.4 us. 11 chunks of up to 701 fp32 tokens (12 heads on 3, d = 64) 14 us.
 #include <algorithm>
 
 #include "q8_attend.cuh"

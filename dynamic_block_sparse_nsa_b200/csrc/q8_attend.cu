@@ -28,6 +28,16 @@
 // reads 16 bytes of key g (K: 16 components, the product's k index permuted
 // the same way in q) or the same 16 components of four keys (V), so no
 // transposition is needed; the slots' swizzles make both conflict-free.
+//
+// Measured, 64 query heads on 4 KV heads, d = 128, bf16: one query of each of 32
+// sequences of 65536 tokens 330 us, 6.5 TB/s of codes, the rate of a copy; in
+// long runs of such calls 392 us, at the board's power limit. A short call is
+// one or two passes of a warp (some 4250 instructions, no loop to warm the
+// instruction cache) between start and join: 1000 tokens 14.6 us, of 0.16 for
+// the bytes. fp32 does each product twice and splits every p: 24 sequences of up
+// to 9001 tokens (40 heads on 8, d = 64) 54 us of 17. What was measured slower:
+// prefetches of pages into L2 (518 us), chunks of 32 keys (531 us), twelve warps
+// a block (fp32 64 us), one copy of the loop's body for both kinds of chunk (350).
 #include <algorithm>
 
 #include "q8_attend.cuh"
