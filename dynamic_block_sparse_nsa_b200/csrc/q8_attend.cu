@@ -1108,14 +1108,17 @@ __device__ __forceinline__ I block_scan(I mine, I* sums, I& total) {
   }
   if (lane == 31) sums[warp] = run;
   __syncthreads();
-  I before = 0;
-  total = 0;
-  for (int k = 0; k < kPlanThreads / 32; ++k) {
-    if (k < warp) before += sums[k];
-    total += sums[k];
+  static_assert(kPlanThreads == 32 * 32, "a lane for each warp's sum");
+  I all = sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I up = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += up;
   }
+  total = __shfl_sync(0xffffffffu, all, 31);
+  const I before = __shfl_sync(0xffffffffu, all, (warp + 31) % 32);
   __syncthreads();
-  return before + run - mine;
+  return (warp ? before : I(0)) + run - mine;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) q8_plan_kernel(const Q8AttendArgs a, int tile_rows,
@@ -1245,6 +1248,13 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
   a.rt = (a.G + ROWS - 1) / ROWS;
   a.blocks = std::min(device_sm_count(), kQ8MaxBlocks);
   a.min_chunks = 8;
+  a.plan_pre = nullptr;
+  a.plan_seq = nullptr;
+  a.plan_base = nullptr;
+  // Chunks of queries on the tensor-memory kernel once a sequence has rows to
+  // fill a good part of its 128-row tiles with; below that most of the tile is
+  // padding, and the kernel here reads the same codes once per 16 rows.
+  const bool tc = ragged && q8_prefill_tc_shape(p) && (long)a.N * a.G >= 32l * p.B;
   // Units of few chunks: whole ones to a block, which leaves no partials and
   // saves the merge kernel (3 to 6 us; a pass of a block's warps over a chunk
   // each takes 2 us). With the most chunks a unit can have, that may cost 1.25
@@ -1257,18 +1267,12 @@ cudaError_t launch_q8_attend(const nsa_params& p, Q8AttendArgs a, void* ws, cuda
                                                 : ((long)a.T + CK - 1) / CK;
   const long units = (long)a.tiles * a.Hkv, per = (units + a.blocks - 1) / a.blocks;
   const double even = (double)units * most / (kWarps * (double)a.blocks);
-  a.by_unit = most > kUnitChunks || per * most > kWarps * (std::max(1.0, even) + 1.25) ? 0
-              : a.keys == q8::KEYS_ALL && units > a.blocks                             ? 2
-                                                                                       : 1;
-  if (a.by_unit) a.blocks = (int)std::min<long>(a.blocks, units);
-  a.plan_pre = nullptr;
-  a.plan_seq = nullptr;
-  a.plan_base = nullptr;
-  // Chunks of queries on the tensor-memory kernel once a sequence has rows to
-  // fill a good part of its 128-row tiles with; below that most of the tile is
-  // padding, and the kernel here reads the same codes once per 16 rows.
-  const bool tc = ragged && q8_prefill_tc_shape(p) && (long)a.N * a.G >= 32l * p.B;
-  // (and its two halves share the keys where most sequences have rows for one)
+  a.by_unit = 0;
+  if (!tc && most <= kUnitChunks && per * most <= kWarps * (std::max(1.0, even) + 1.25)) {
+    a.by_unit = a.keys == q8::KEYS_ALL && units > a.blocks ? 2 : 1;
+    a.blocks = (int)std::min<long>(a.blocks, units);
+  }
+  // (its two halves share the keys where most sequences have rows for one)
   const bool split = tc && (long)a.N * a.G <= kQ8TcRows / 2 * (long)p.B;
   if (tc) a.tiles = (int)((long)a.N * a.G / kQ8TcRows + p.B);
   if (ragged || a.tiles > kSmemTiles) {
