@@ -15,11 +15,12 @@
 // calls and by latency for one token per sequence. A (page, head) of K or V is
 // one block's work: its rows stay in registers between the maximum and the
 // codes, so nothing is read from memory twice. Query rows have a kernel of their
-// own ahead of it, which the pages' blocks overlap. With one token per sequence a
+// own ahead of it, which the pages' blocks overlap, or blocks behind the pages'
+// where they are few. With one token per sequence a
 // warp takes a (sequence, head) of K or V instead, and more warps the query rows.
 // Measured, 64 query heads on 4 KV heads, d = 128, bf16: 8192 tokens 64 us, 4.9
 // TB/s in and out (loads in flight bound the query rows); 32 sequences of a token
-// each 3.4 us. 11 chunks of up to 701 fp32 tokens (12 heads on 3, d = 64) 14 us.
+// each 3.4 us. 11 chunks of up to 701 fp32 tokens (12 heads on 3, d = 64) 13 us.
 #include <algorithm>
 
 #include "q8_attend.cuh"
@@ -30,6 +31,7 @@ namespace {
 using q8::Vec8;
 
 constexpr int kThreads = 256;
+constexpr int kTogether = 2048;  // most blocks of query rows that share the pages' launch
 
 // The two 8-component pieces of a row that thread j of its d / 16 owns: with
 // pairs (i, i + rot / 2) they are each other's partners, behind the rotated
@@ -251,10 +253,9 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
 // rows a thread at fewer blocks an SM: 70 us for a call of 8192 tokens with 64
 // heads, against 64).
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads, 5) q8_append_query_kernel(Q8AppendArgs a, int tokens) {
-  ptx::grid_dep_launch();  // (the pages' kernel needs nothing from here)
+__device__ __forceinline__ void query_rows(const Q8AppendArgs& a, int tokens, int block) {
   const int tpr = a.d / 16, rpp = kThreads / tpr, j = threadIdx.x % tpr;
-  const int t0 = blockIdx.x * tokens;
+  const int t0 = block * tokens;
   const int rows = min(tokens, a.N - t0) * a.Hq;
   int token = -1, at = -1;  // of the row before: a token's heads share them
   for (int r = threadIdx.x / tpr; r < rows; r += rpp) {
@@ -273,10 +274,22 @@ __global__ void __launch_bounds__(kThreads, 5) q8_append_query_kernel(Q8AppendAr
   }
 }
 
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads, 5) q8_append_query_kernel(Q8AppendArgs a, int tokens) {
+  ptx::grid_dep_launch();  // (the pages' kernel needs nothing from here)
+  query_rows<T, HALF>(a, tokens, blockIdx.x);
+}
+
 // K and V of a call with offsets: a block per (page of a sequence's new tokens,
-// KV head, K or V). NP: passes of the block's threads over a page's rows.
+// KV head, K or V). NP: passes of the block's threads over a page's rows. Of a
+// short call the blocks from `pages` on rotate the query rows.
 template <typename T, bool HALF, int NP>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a) {
+__global__ void __launch_bounds__(kThreads) q8_append_kernel(Q8AppendArgs a, unsigned pages,
+                                                             int tokens) {
+  if (blockIdx.x >= pages) {
+    query_rows<T, HALF>(a, tokens, blockIdx.x - pages);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tpr = a.d / 16, rpp = kThreads / tpr;
   const int j = tid % tpr;
@@ -416,10 +429,15 @@ cudaError_t launch(const Q8AppendArgs& a, cudaStream_t stream) {
     q8_append_step_kernel<T, HALF><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  if (a.q) {
-    // two rounds of a block's rows, or one token's heads
-    const int tokens = std::max(1, 2 * (kThreads / tpr) / a.Hq);
-    const int blocks = (a.N + tokens - 1) / tokens;
+  // two rounds of a block's query rows, or one token's heads
+  const int tokens = std::max(1, 2 * (kThreads / tpr) / a.Hq);
+  const int blocks = a.q ? (a.N + tokens - 1) / tokens : 0;
+  // Few of them: one launch for both kinds of blocks (64 query heads, d = 128: 1000
+  // tokens 9.4 us against 11.3, and 2 us less on the host; 2000 tokens 16.9 and
+  // 17.4; 3000 tokens 29.8 and 27.2, for the pages' registers leave fewer blocks
+  // of query rows on an SM).
+  const bool together = blocks <= kTogether;
+  if (!together) {
     TraceScope trace("append_q8_query", stream);
     q8_append_query_kernel<T, HALF><<<blocks, kThreads, 0, stream>>>(a, tokens);
     const cudaError_t e = cudaGetLastError();
@@ -432,9 +450,9 @@ cudaError_t launch(const Q8AppendArgs& a, cudaStream_t stream) {
               : passes == 2 ? q8_append_kernel<T, HALF, 2>
                             : q8_append_kernel<T, HALF, 4>;
   TraceScope trace("append_q8", stream);
-  if (a.q)
-    return q8::launch_pdl(kern, dim3((unsigned)(items * a.Hkv * 2)), dim3(kThreads), 0, stream, a);
-  kern<<<(unsigned)(items * a.Hkv * 2), kThreads, 0, stream>>>(a);
+  const unsigned pages = (unsigned)(items * a.Hkv * 2);
+  if (!together) return q8::launch_pdl(kern, dim3(pages), dim3(kThreads), 0, stream, a, pages, tokens);
+  kern<<<pages + blocks, kThreads, 0, stream>>>(a, pages, tokens);
   return cudaGetLastError();
 }
 

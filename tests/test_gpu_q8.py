@@ -219,6 +219,32 @@ def test_append_token_by_token_equals_one_call():
     assert torch.equal(one.k_scale, steps.k_scale)
 
 
+@pytest.mark.parametrize("dt", (BF16, F32))
+def test_append_long_call_equals_short_ones(dt):
+    """A call whose query rows have a launch of their own, against calls that do not."""
+    N, cut = 2500, 1280  # (the cut between two pages)
+    p = nsa.params(1, N, 64, 1, 128, dtype=dt)
+    table = torch.randperm(40, generator=gen(81)).to(torch.int32)[None].cuda()
+    rope = nsa.rope_table(N, 128)
+    g = gen(82)
+    k, v = (torch.randn(N, 1, 128, generator=g).to(dt).cuda() for _ in range(2))
+    q = torch.randn(N, 64, 128, generator=g).to(dt).cuda()
+    one, two = nsa.q8_cache(p, 40, table), nsa.q8_cache(p, 40, table)
+    whole = nsa.nsa_append_q8(p, k, v, i32([0]), one, i32([0, N]), q, rope, want_kv=True)
+    for lo, hi in ((0, cut), (cut, N)):
+        part = nsa.nsa_append_q8(p, k[lo:hi], v[lo:hi], i32([lo]), two, i32([0, hi - lo]), q[lo:hi],
+                                 rope, want_kv=True)
+        nsa.nsa_check()
+        for x, y in zip(whole, part):
+            assert torch.equal(x[lo:hi], y)
+    for x, y in ((one.k_pages, two.k_pages), (one.v_pages, two.v_pages)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert torch.equal(one.k_scale, two.k_scale) and torch.equal(one.v_scale, two.v_scale)
+    turned = ref.turned(q.cpu().double(), rope, torch.arange(N), "half")
+    lim = 2.0 ** -20 * q.abs().max().item() + turned.abs() * (2.0 ** -8 if dt == BF16 else 2.0 ** -24)
+    assert ((whole[0].cpu().double() - turned).abs() <= lim).all()
+
+
 def test_append_many_sequences():
     """More sequences than a block's threads, many without new tokens."""
     B = 700
