@@ -63,6 +63,15 @@ __device__ __forceinline__ void turn_of(float (&cs)[16], const Q8AppendArgs& a, 
   }
 }
 
+// Rotates a pair. The products are rounded apart, not fused into the sum: any
+// fp32 evaluation of the formula then gives the same key, and the same code where
+// it lies near the middle of two.
+__device__ __forceinline__ void turn_pair(float& u, float& v, float c, float s) {
+  const float a = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
+  v = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
+  u = a;
+}
+
 // Rotates the 16 components x = [piece a, piece b] of a row.
 template <bool HALF>
 __device__ __forceinline__ void rotate(float (&x)[16], const float (&cs)[16],
@@ -70,18 +79,10 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float (&cs)[16],
   if (j >= a.rot / 16) return;
   if (HALF) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = x[i], v = x[8 + i];
-      x[i] = u * cs[i] - v * cs[8 + i];
-      x[8 + i] = v * cs[i] + u * cs[8 + i];
-    }
+    for (int i = 0; i < 8; ++i) turn_pair(x[i], x[8 + i], cs[i], cs[8 + i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = x[2 * i], v = x[2 * i + 1];
-      x[2 * i] = u * cs[i] - v * cs[8 + i];
-      x[2 * i + 1] = v * cs[i] + u * cs[8 + i];
-    }
+    for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], cs[i], cs[8 + i]);
   }
 }
 
