@@ -18,7 +18,11 @@
 // spread of scales over the pages can push it out of fp16's range, the output
 // has a running reference of its own: o is kept in units of 2^M with M the
 // largest m_page + log2(vscale) so far (less 10, which puts p * vscale in
-// (0, 1024] and its smallest normal 2^-24 below the largest).
+// (0, 1024] and its smallest normal 2^-24 below the largest). A scale says
+// little of what a row sees: it may be that of a later token, of one before the
+// window, or of one written over since. So once the scales of a warp's pages lie
+// more than 2^8 apart, M is the largest p * max |v| of a single key instead, and
+// falls to what o holds where an earlier page had set it too high (apart_softmax).
 //
 // Each warp streams its own contiguous share of the chunks (64 keys) through a
 // private ring of three cp.async slots, each K or V of a chunk, two of them in
@@ -57,6 +61,8 @@ constexpr int ROWS = 16;     // query rows per tile
 constexpr int kUnitChunks = 4 * kWarps;  // most chunks of a unit that one block takes whole
 constexpr int SLOTS = 3;     // of a warp's ring
 constexpr int kSmemTiles = 1024;  // tiles whose prefix a block computes itself
+constexpr int kFar = 1 << 20;     // beyond every scale's exponent
+constexpr int kAbsent = INT_MAX / 2;  // first key of an absent page: past every row
 
 template <int D>
 struct Geo {
@@ -176,7 +182,6 @@ struct Feeder {
   int cp[PP], ckb[PP], coff;  // the chunk's pages, their first keys, the first key's slot
   int centry;                 // and its first entry
   bool whole;                 // every row of the chunk is a live key
-
   __device__ __forceinline__ void pages(const Q8AttendArgs& a, int e, int lane) {
     gbase = e;
     const int i = e + lane;
@@ -233,7 +238,7 @@ struct Feeder {
       const int src = e - gbase + i;
       cp[i] = __shfl_sync(0xffffffffu, pid, src);
       ckb[i] = __shfl_sync(0xffffffffu, blk, src) * a.page + coff;
-      if (cp[i] < 0) ckb[i] = INT_MAX / 2;  // past every row
+      if (cp[i] < 0) ckb[i] = kAbsent;
       some |= ckb[i] < u.hi && ckb[i] + w > u.lo;
       full &= ckb[i] >= full_lo && ckb[i] + w <= full_hi;
       whole &= ckb[i] >= u.lo && ckb[i] + w <= u.hi;
@@ -254,6 +259,24 @@ struct Feeder {
         meta->vs[i] = v;
       }
     }
+  }
+
+  // Whether the value scales of the unit's pages lie far apart, those just looked
+  // up among them. `range`: the warp's, log2 of the least and the largest so far.
+  __device__ __forceinline__ bool far(int* range, bool begun, int lane) const {
+    const int level = __float2int_rd(__log2f(vs));
+    int low = __reduce_min_sync(0xffffffffu, pid >= 0 && level > (int)q8::kSmall ? level : kFar);
+    int high = __reduce_max_sync(0xffffffffu, pid >= 0 ? level : -kFar);
+    if (begun) {
+      low = min(low, range[0]);
+      high = max(high, range[1]);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      range[0] = low;
+      range[1] = high;
+    }
+    return high - low > (int)q8::kSpread;
   }
 
   // Copies K or V of the chunk into a slot.
@@ -430,21 +453,116 @@ struct Rows {
     }
   }
 
+  template <int PP>
+  __device__ __forceinline__ void mask(float (&z)[NS][4], const ChunkMeta<PP>& meta, int lane) const {
+    const int t = lane & 3;
+    constexpr int TP = NS / PP;
+#pragma unroll
+    for (int nt = 0; nt < NS; ++nt)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int key = meta.kb[nt / TP] + 8 * (nt % TP) + t + 4 * (x & 1);
+        if (key < lo[x >> 1] || key >= hi[x >> 1]) z[nt][x] = -INFINITY;
+      }
+  }
+
+  // code_room of the values of key r of a slot; NaN codes do not count.
+  static __device__ __forceinline__ uint32_t room_of(const unsigned char* vst, int r, int lane) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const uint4 v = *reinterpret_cast<const uint4*>(vst + r * D + (c + lane) % (D / 16) * 16);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u = w[i] & 0x7f7f7f7fu;
+        top = __vmaxu4(top, u & ~__vcmpeq4(u, 0x7f7f7f7fu));
+      }
+    }
+    top = max(top & 0xffffu, top >> 16);
+    return q8::code_room(max(top & 0xffu, top >> 8));
+  }
+
+  // The running softmax of a chunk in a unit whose value scales lie far apart. M is
+  // the largest z2 + log2(vscale) - room of a key with values other than zero (less
+  // 10), and what o holds; it may fall. p and p * vscale are exponentials of their
+  // own: one may vanish and the other not.
+  template <int PP>
+  __device__ __forceinline__ void apart_softmax(float (&z)[NS][4], const ChunkMeta<PP>& meta,
+                                                bool full, const unsigned char* vst, int lane) {
+    const int t = lane & 3;
+    constexpr int TP = NS / PP;
+    if (!full) mask<PP>(z, meta, lane);
+    float lv[PP];
+#pragma unroll
+    for (int p = 0; p < PP; ++p) lv[p] = __log2f(meta.vs[p]);
+    uint32_t room[2] = {0, 0};  // of keys t, 8 + t, ..; 4 + t, 12 + t, ..: four bits each
+    {
+      const uint32_t a = room_of(vst, lane, lane), b = room_of(vst, lane + 32, lane);
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          room[y] |= __shfl_sync(0xffffffffu, nt < NS / 2 ? a : b, (8 * nt + t + 4 * y) % 32) << 4 * nt;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = m[i], ref = -INFINITY, most_o = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt) {
+        const float c = fmaxf(qf[i] * meta.ks[nt / TP], 1.17549435e-38f);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t r = room[y] >> 4 * nt & 15u;
+          z[nt][2 * i + y] = __fmul_rn(z[nt][2 * i + y], c);
+          top = fmaxf(top, z[nt][2 * i + y]);
+          if (r != q8::kNoCode)
+            ref = fmaxf(ref, z[nt][2 * i + y] + fmaxf(lv[nt / TP], -126.f) - (float)(r + 10u));
+        }
+      }
+      top = quad_max(top);
+      ref = quad_max(ref);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        most_o = fmaxf(most_o, fmaxf(fabsf(o[j][2 * i]), fabsf(o[j][2 * i + 1])));
+      most_o = quad_max(most_o);
+      const float before = M[i];
+      M[i] = q8::apart_reference(before, ref, most_o);
+      if (__any_sync(0xffffffffu, most_o > 0.f && M[i] != before)) {
+        // in two factors: M may fall by more than fp32's range
+        const float half = most_o > 0.f ? ptx::ex2(0.5f * (before - M[i])) : 1.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][2 * i] = o[j][2 * i] * half * half;
+          o[j][2 * i + 1] = o[j][2 * i + 1] * half * half;
+        }
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      const float oref = M[i] == -INFINITY ? 0.f : M[i];
+      const float al = ptx::ex2(m[i] - base);
+      m[i] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float d = __fadd_rn(z[nt][2 * i + y], -base);
+          sum += ptx::ex2(d);
+          // (values of zeros or NaN: any finite weight does)
+          z[nt][2 * i + y] = (room[y] >> 4 * nt & 15u) == q8::kNoCode
+                                 ? 0.f
+                                 : ptx::ex2(d + (base - oref + lv[nt / TP]));
+        }
+      l[i] = l[i] * al + sum;
+    }
+  }
+
   // Running softmax: z becomes p * vscale in units of 2^M; o, l, m, M follow.
   template <int PP>
   __device__ __forceinline__ void softmax(float (&z)[NS][4], const ChunkMeta<PP>& meta, bool full,
                                           int lane) {
-    const int t = lane & 3;
     constexpr int TP = NS / PP;  // score tiles of a page
-    if (!full) {
-#pragma unroll
-      for (int nt = 0; nt < NS; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = meta.kb[nt / TP] + 8 * (nt % TP) + t + 4 * (x & 1);
-          if (key < lo[x >> 1] || key >= hi[x >> 1]) z[nt][x] = -INFINITY;
-        }
-    }
+    if (!full) mask<PP>(z, meta, lane);
     float lv[PP];  // log2 of the value scales
 #pragma unroll
     for (int p = 0; p < PP; ++p) lv[p] = __log2f(meta.vs[p]);
@@ -475,8 +593,8 @@ struct Rows {
       for (int p = 0; p < PP; ++p) apart |= !(base - oref + lv[p] > -60.f);
       if (__any_sync(0xffffffffu, apart)) {
         // p for itself, from a rounded score: a page of far smaller values than
-        // the others', whose p * vscale vanishes and p does not; or scores so
-        // large that the exact z2 - m of a fused product is not 0 at the maximum
+        // the others' (kSmall), whose p * vscale vanishes and p does not; or scores
+        // so large that the exact z2 - m of a fused product is not 0 at the maximum
 #pragma unroll
         for (int nt = 0; nt < NS; ++nt)
 #pragma unroll
@@ -738,7 +856,8 @@ template <typename T, int D, int PP>
 struct Smem {
   static constexpr int RING = kWarps * Geo<D>::RING;
   static constexpr int META = RING;
-  static constexpr int SEGS = (META + kWarps * 2 * (int)sizeof(ChunkMeta<PP>) + 15) / 16 * 16;
+  static constexpr int RANGE = META + kWarps * 2 * (int)sizeof(ChunkMeta<PP>);
+  static constexpr int SEGS = (RANGE + kWarps * 8 + 15) / 16 * 16;
   static constexpr int LSE = SEGS + kSegs * (int)sizeof(Segment);  // of the segments' rows
   static constexpr int WGT = LSE + kSegs * ROWS * 4;               // their weights in the join
   static constexpr int SUMS = WGT + kSegs * ROWS * 4;
@@ -747,7 +866,145 @@ struct Smem {
   static constexpr int BYTES = LENS + kSmemTiles * 4;
 };
 
-// MULTI: a tile can hold several tokens, which see different keys.
+// A warp's share of the chunks, [x0, x1). MULTI: a tile can hold several tokens,
+// which see different keys. FAR: apart_softmax for all of them; without, false at
+// the first sight of a unit whose value scales lie far apart, the share undone.
+template <typename T, int D, int PP, bool MULTI, bool FAR>
+__device__ __forceinline__ bool share(const Q8AttendArgs& a, const Plan& pl, unsigned char* smem,
+                                      int cta, long x0, long x1) {
+  using S = Smem<T, D, PP>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
+  float* seg_lse = reinterpret_cast<float*>(smem + S::LSE);
+  constexpr int TILE = Geo<D>::TILE;
+  unsigned char* ring = smem + warp * Geo<D>::RING;
+  ChunkMeta<PP>* meta = reinterpret_cast<ChunkMeta<PP>*>(smem + S::META) + warp * 2;
+  int* range = reinterpret_cast<int*>(smem + S::RANGE) + warp * 2;
+  const uint32_t ring_u = ptx::smem_u32(ring);
+  Feeder<D, PP> feed;
+  feed.start(a, pl, x0);
+  Place at = feed.at;
+  Unit u = feed.u;
+  Rows<T, D> rows;
+  {
+    typename Rows<T, D>::Raw raw;
+    rows.fetch(raw, a, u, at.h, lane);
+    // K and V of the first chunk into slots 0 and 1
+    feed.look(a, meta, lane);
+    feed.template copy<false>(a, ring_u, lane);
+    ptx::cp_async_commit();
+    feed.template copy<true>(a, ring_u + TILE, lane);
+    ptx::cp_async_commit();
+    rows.load(raw, a, u, lane);
+    feed.scales(meta, lane);
+    if (!FAR && feed.far(range, false, lane)) {
+      ptx::cp_async_wait<0>();  // (the ring is used anew)
+      __syncwarp();
+      return false;
+    }
+  }
+  rows.clear();
+  bool whole = at.c == 0;  // the unit's first chunk is the warp's
+  int sk = 0;              // slot of the chunk's K; its V is in the next, the next K behind that
+  int mi = 0;
+  const int len = (int)(x1 - x0);
+  for (int x = 0; x < len; ++x) {
+    const int sv = sk + 1 == SLOTS ? 0 : sk + 1, sn = sv + 1 == SLOTS ? 0 : sv + 1;
+    ptx::cp_async_wait<1>();  // K
+    __syncwarp();
+    const bool more = x + 1 < len;
+    if (more) {
+      feed.next(a, pl);
+      feed.look(a, meta + (mi ^ 1), lane);
+      feed.template copy<false>(a, ring_u + sn * TILE, lane);
+    }
+    ptx::cp_async_commit();
+    if (more) feed.scales(meta + (mi ^ 1), lane);
+    if (!FAR && more && feed.centry == feed.gbase && feed.far(range, feed.at.c > 0, lane)) {
+      ptx::cp_async_wait<0>();  // (the ring is used anew)
+      __syncwarp();
+      return false;
+    }
+    const ChunkMeta<PP>& sm = meta[mi];
+    const int state = sm.state;
+    float z[NS][4];
+    if (state) {
+      rows.scores(z, ring_u + sk * TILE, lane);
+      if (FAR) {
+        ptx::cp_async_wait<1>();  // V, which the weights go by
+        __syncwarp();
+        rows.template apart_softmax<PP>(z, sm, state == 2, ring + sv * TILE, lane);
+      } else {
+        rows.template softmax<PP>(z, sm, state == 2, lane);
+      }
+    }
+    ptx::cp_async_wait<1>();  // V
+    __syncwarp();
+    if (more) feed.template copy<true>(a, ring_u + sk * TILE, lane);
+    ptx::cp_async_commit();
+    if (state) {
+      if (MULTI && state == 1)
+        rows.template nan_values<PP>(ring + sv * TILE, sm, lane);
+      rows.values(z, ring_u + sv * TILE, lane);
+    }
+    sk = sn;
+    mi ^= 1;
+    const bool last = at.c + 1 == at.nc;
+    if (last || !more) {
+      float lse2[2];
+      rows.finish(lse2);
+      if (whole && last) {
+        rows.write(a, u, at.h, lse2, lane);
+      } else if (more) {
+        float* part = a.hold + ((long)cta * kWarps + warp) * Geo<D>::PART;
+        rows.store(part, seg_lse + 2 * warp * ROWS, lse2, lane);
+        if (lane == 0)
+          segs[2 * warp] = Segment{x0 + x - at.c, at.nc, at.tile, at.h, u.r0, u.s.first, u.s.n, part};
+      } else {
+        ptx::cp_async_wait<0>();
+        __syncwarp();  // the ring is free
+        float* part = reinterpret_cast<float*>(ring);
+        rows.store(part, seg_lse + (2 * warp + 1) * ROWS, lse2, lane);
+        if (lane == 0)
+          segs[2 * warp + 1] =
+              Segment{x0 + x - at.c, at.nc, at.tile, at.h, u.r0, u.s.first, u.s.n, part};
+      }
+      if (more) {
+        const int tile = at.tile;
+        at.next(pl, a.Hkv);
+        if (at.tile != tile) u.load(a, pl, at.tile);
+        typename Rows<T, D>::Raw raw;
+        rows.fetch(raw, a, u, at.h, lane);
+        rows.load(raw, a, u, lane);
+        rows.clear();
+        whole = true;
+      }
+    } else {
+      ++at.c;
+    }
+  }
+  return true;
+}
+
+// The plan: that of the launch before, or the block's own (made in shared memory).
+template <typename T, int D, int PP>
+__device__ __forceinline__ Plan plan_of(const Q8AttendArgs& a, unsigned char* smem) {
+  using S = Smem<T, D, PP>;
+  if (a.plan_pre)
+    return Plan{a.plan_pre, a.plan_seq, a.plan_base, nullptr, a.plan_base[a.B], a.rt};
+  return Plan{reinterpret_cast<long*>(smem + S::PRE), nullptr, nullptr,
+              reinterpret_cast<int*>(smem + S::LENS), a.tiles, a.rt};
+}
+
+// share of a warp with FAR: a call, so that it takes no registers from the other.
+template <typename T, int D, int PP, bool MULTI>
+__device__ __noinline__ void share_far(const Q8AttendArgs& a, unsigned char* smem, int cta, long X0,
+                                       long X1) {
+  const int warp = threadIdx.x >> 5;
+  share<T, D, PP, MULTI, true>(a, plan_of<T, D, PP>(a, smem), smem, cta,
+                               X0 + (X1 - X0) * warp / kWarps, X0 + (X1 - X0) * (warp + 1) / kWarps);
+}
+
 template <typename T, int D, int PP, bool MULTI>
 __global__ void __launch_bounds__(kThreads, 1)
     q8_attend_kernel(const __grid_constant__ Q8AttendArgs a) {
@@ -761,18 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::grid_dep_launch();
 
   // ---- plan ----
-  Plan pl;
-  pl.tiles = a.tiles;
-  pl.rt = a.rt;
-  pl.tseq = nullptr;
-  pl.tbase = nullptr;
-  pl.lens = nullptr;
-  if (a.plan_pre) {
-    pl.pre = a.plan_pre;
-    pl.tseq = a.plan_seq;
-    pl.tbase = a.plan_base;
-    pl.tiles = a.plan_base[a.B];
-  } else {
+  if (!a.plan_pre) {
     long* pre = reinterpret_cast<long*>(smem + S::PRE);
     long* sums = reinterpret_cast<long*>(smem + S::SUMS);
     int* lens = reinterpret_cast<int*>(smem + S::LENS);
@@ -805,9 +1051,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tile < a.tiles) pre[tile + 1] = before + run;
       __syncthreads();
     }
-    pl.pre = pre;
-    pl.lens = lens;
   }
+  const Plan pl = plan_of<T, D, PP>(a, smem);
   if (tid < kSegs) segs[tid].nc = 0;
   __syncthreads();
   const long V = pl.tiles ? pl.pre[pl.tiles] : 0;
@@ -829,98 +1074,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const long x0 = X0 + (X1 - X0) * warp / kWarps, x1 = X0 + (X1 - X0) * (warp + 1) / kWarps;
 
-  if (x1 > x0) {
-    constexpr int TILE = Geo<D>::TILE;
-    unsigned char* ring = smem + warp * Geo<D>::RING;
-    ChunkMeta<PP>* meta = reinterpret_cast<ChunkMeta<PP>*>(smem + S::META) + warp * 2;
-    const uint32_t ring_u = ptx::smem_u32(ring);
-    Feeder<D, PP> feed;
-    feed.start(a, pl, x0);
-    Place at = feed.at;
-    Unit u = feed.u;
-    Rows<T, D> rows;
-    {
-      typename Rows<T, D>::Raw raw;
-      rows.fetch(raw, a, u, at.h, lane);
-      // K and V of the first chunk into slots 0 and 1
-      feed.look(a, meta, lane);
-      feed.template copy<false>(a, ring_u, lane);
-      ptx::cp_async_commit();
-      feed.template copy<true>(a, ring_u + TILE, lane);
-      ptx::cp_async_commit();
-      rows.load(raw, a, u, lane);
-      feed.scales(meta, lane);
-    }
-    rows.clear();
-    bool whole = at.c == 0;  // the unit's first chunk is the warp's
-    int sk = 0;              // slot of the chunk's K; its V is in the next, the next K behind that
-    int mi = 0;
-    const int len = (int)(x1 - x0);
-    for (int x = 0; x < len; ++x) {
-      const int sv = sk + 1 == SLOTS ? 0 : sk + 1, sn = sv + 1 == SLOTS ? 0 : sv + 1;
-      ptx::cp_async_wait<1>();  // K
-      __syncwarp();
-      const bool more = x + 1 < len;
-      if (more) {
-        feed.next(a, pl);
-        feed.look(a, meta + (mi ^ 1), lane);
-        feed.template copy<false>(a, ring_u + sn * TILE, lane);
-      }
-      ptx::cp_async_commit();
-      if (more) feed.scales(meta + (mi ^ 1), lane);
-      const ChunkMeta<PP>& sm = meta[mi];
-      const int state = sm.state;
-      float z[NS][4];
-      if (state) {
-        rows.scores(z, ring_u + sk * TILE, lane);
-        rows.template softmax<PP>(z, sm, state == 2, lane);
-      }
-      ptx::cp_async_wait<1>();  // V
-      __syncwarp();
-      if (more) feed.template copy<true>(a, ring_u + sk * TILE, lane);
-      ptx::cp_async_commit();
-      if (state) {
-        if (MULTI && state == 1)
-          rows.template nan_values<PP>(ring + sv * TILE, sm, lane);
-        rows.values(z, ring_u + sv * TILE, lane);
-      }
-      sk = sn;
-      mi ^= 1;
-      const bool last = at.c + 1 == at.nc;
-      if (last || !more) {
-        float lse2[2];
-        rows.finish(lse2);
-        if (whole && last) {
-          rows.write(a, u, at.h, lse2, lane);
-        } else if (more) {
-          float* part = a.hold + ((long)cta * kWarps + warp) * Geo<D>::PART;
-          rows.store(part, seg_lse + 2 * warp * ROWS, lse2, lane);
-          if (lane == 0)
-            segs[2 * warp] = Segment{x0 + x - at.c, at.nc, at.tile, at.h, u.r0, u.s.first, u.s.n, part};
-        } else {
-          ptx::cp_async_wait<0>();
-          __syncwarp();  // the ring is free
-          float* part = reinterpret_cast<float*>(ring);
-          rows.store(part, seg_lse + (2 * warp + 1) * ROWS, lse2, lane);
-          if (lane == 0)
-            segs[2 * warp + 1] =
-                Segment{x0 + x - at.c, at.nc, at.tile, at.h, u.r0, u.s.first, u.s.n, part};
-        }
-        if (more) {
-          const int tile = at.tile;
-          at.next(pl, a.Hkv);
-          if (at.tile != tile) u.load(a, pl, at.tile);
-          typename Rows<T, D>::Raw raw;
-          rows.fetch(raw, a, u, at.h, lane);
-          rows.load(raw, a, u, lane);
-          rows.clear();
-          whole = true;
-        }
-      } else {
-        ++at.c;
-      }
-    }
-  }
+  if (x1 > x0 && !share<T, D, PP, MULTI, false>(a, pl, smem, cta, x0, x1))
+    share_far<T, D, PP, MULTI>(a, smem, cta, X0, X1);
   __syncthreads();
 
   // ---- join the block's segments of each unit ----

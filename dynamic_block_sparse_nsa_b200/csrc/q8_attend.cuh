@@ -25,6 +25,30 @@ enum { KEYS_ALL = NSA_KEYS_ALL, KEYS_WINDOW = NSA_KEYS_WINDOW, KEYS_BLOCKS = NSA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Value scales of a unit's pages that lie further apart than 2^kSpread ("far
+// apart"): the output's reference M is then taken from the codes that a row sees
+// and from its sums, not from the scales, which other tokens may have set. Scales
+// up to 2^kSmall do not count: no value under them reaches 1e-30.
+constexpr float kSpread = 8.f, kSmall = -109.f;
+
+// Places, 0 to 5, by which the largest magnitude c of a key's value codes lies
+// below 2^8: a weight may be that much larger beside it in fp16. kNoCode: zeros.
+constexpr uint32_t kNoCode = 7u;
+__device__ __forceinline__ uint32_t code_room(uint32_t c) {
+  return c == 0u ? kNoCode : min(5u, 15u - (c >> 3));
+}
+
+// The reference M of a row in such a unit, from its value so far, what the chunk's
+// keys ask for (ref: their weights are then at most 2^15) and the largest magnitude
+// of the row's sums, in units of 2^M (a key's product is at most 2^19): it falls no
+// lower than they reach. A whole number, so that sums follow it exactly.
+__device__ __forceinline__ float apart_reference(float M, float ref, float sums) {
+  const float held = sums > 0.f ? M + fminf(log2f(sums) - 19.f, 0.f) : -INFINITY;
+  const float want = fmaxf(ref, held);
+  if (want == -INFINITY || (want <= M && want > M - 4.f)) return M;
+  return ceilf(want);
+}
+
 // Tiles of sequence b, its first query row, queries and length. A length that
 // is out of range (or shorter than the queries) gives ok = false: its rows
 // have no keys.

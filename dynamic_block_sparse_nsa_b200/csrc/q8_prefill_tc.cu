@@ -52,6 +52,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLag = 5.f;        // how far M may fall behind before O is rescaled
 constexpr int kRing = 3;           // fp16 tiles: K of chunk 0, V of it, K of chunk 1, ...
 constexpr int kRaw = 3;            // tiles of codes under way
+constexpr int kFar = 1 << 20;      // beyond every scale's exponent
 constexpr int kNanSlots = 4;       // units whose NaN marks are under way
 // Floats of a partial: o as [D / 4][ROWS] of 4 components (a thread has a row: a
 // warp's stores are contiguous), then lse2 of the rows.
@@ -614,6 +615,126 @@ struct Softmax {
     return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
   }
 
+  // The lane's four keys' code_room (q8_attend.cuh), a byte each, from the fp16 V
+  // tile: a row's largest magnitude.
+  static __device__ __forceinline__ uint32_t rooms_of(const unsigned char* tile, int lane) {
+    uint32_t rooms = 0;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const unsigned char* from = tile + (4 * lane + k) * 128;
+      __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {  // (a row's pieces in any order: lanes on banks of their own)
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(from + (c >> 3) * ATOM + (((c + lane) & 7) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+      }
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&top);
+      const uint32_t c = max(u & 0xffffu, u >> 16);  // a code's exponent is 8 less in fp16
+      const uint32_t room = c == 0u ? q8::kNoCode : min(5u, 23u - (c >> 10));
+      rooms |= room << 8 * k;
+    }
+    return rooms;
+  }
+
+  // A chunk's softmax in a unit whose value scales lie far apart: that of
+  // q8_attend.cu's apart_softmax. `sc`, `oc`: S and O of the warp's rows, lo and hi
+  // count from the chunk's first key, `tile` is its V.
+  struct Sums {
+    float m, M, l;
+  };
+  static __device__ __forceinline__ Sums apart_softmax(uint32_t sc, uint32_t oc, int pid, float ks,
+                                                    float vlog, int shift, float qf, int lo, int hi,
+                                                    const unsigned char* tile, bool begun, float m,
+                                                    float M, float l) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t rooms = rooms_of(tile, lane);
+    float top = m, ref = -INFINITY, most = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+      uint32_t y[16], rw[4];
+      tc::ld16_sync(sc + 16 * g, y);
+      const int src = (16 * g) >> shift;
+      const float cg = fmaxf(qf * __shfl_sync(0xffffffffu, ks, src), 1.17549435e-38f);
+      const float lg = fmaxf(__shfl_sync(0xffffffffu, vlog, src), -126.f);
+      const bool there = __shfl_sync(0xffffffffu, pid, src) >= 0;
+      const int from = there ? lo - 16 * g : 16, to = hi - 16 * g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rw[k] = __shfl_sync(0xffffffffu, rooms, 4 * g + k);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (e < from || e >= to) continue;
+        const float x = __fmul_rn(__uint_as_float(y[e]), cg);
+        const uint32_t room = rw[e >> 2] >> 8 * (e & 3) & 7u;
+        top = fmaxf(top, x);
+        if (room != q8::kNoCode) ref = fmaxf(ref, x + lg - (float)(room + 10u));
+      }
+    }
+    if (begun) {
+#pragma unroll 1
+      for (int q4 = 0; q4 < 8; ++q4) {
+        uint32_t o[16];
+        tc::ld16_sync(oc + 16 * q4, o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(__uint_as_float(o[e])));
+      }
+    }
+    const float before = M;
+    M = q8::apart_reference(before, ref, most);
+    if (__any_sync(0xffffffffu, most > 0.f && M != before)) {
+      // in two factors: M may fall by more than fp32's range
+      const float half = most > 0.f ? ptx::ex2(0.5f * (before - M)) : 1.f;
+#pragma unroll 1
+      for (int q4 = 0; q4 < 8; ++q4) {
+        uint32_t o[16];
+        tc::ld16_sync(oc + 16 * q4, o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * half * half);
+        tc::st16(oc + 16 * q4, o);
+      }
+    }
+    const float base = top == -INFINITY ? 0.f : top, oref = M == -INFINITY ? 0.f : M;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+      uint32_t y[16], rw[4], p[8];
+      tc::ld16_sync(sc + 16 * g, y);
+      const int src = (16 * g) >> shift;
+      const float cg = fmaxf(qf * __shfl_sync(0xffffffffu, ks, src), 1.17549435e-38f);
+      const float lg = __shfl_sync(0xffffffffu, vlog, src);
+      const bool there = __shfl_sync(0xffffffffu, pid, src) >= 0;
+      const int from = there ? lo - 16 * g : 16, to = hi - 16 * g;
+      const float off = there ? base - oref + lg : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rw[k] = __shfl_sync(0xffffffffu, rooms, 4 * g + k);
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float r[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float d = __fadd_rn(__fmul_rn(__uint_as_float(y[e + k]), cg), -base);
+          const bool seen = e + k >= from && e + k < to;
+          const uint32_t room = rw[e >> 2] >> 8 * ((e + k) & 3) & 7u;
+          sum += seen ? ptx::ex2(d) : 0.f;
+          // (values of zeros or NaN: any finite weight does)
+          r[k] = seen && room != q8::kNoCode ? ptx::ex2(d + off) : 0.f;
+        }
+        p[e / 2] = pack_half(r[0], r[1]);
+      }
+      tc::st8(sc + 8 * g, p);
+    }
+    return Sums{top, M, l * ptx::ex2(m - base) + sum};
+  }
+  static __device__ __noinline__ Sums apart_call(uint32_t sc, uint32_t oc, int pid, float ks,
+                                                 float vlog, int shift, float qf, int lo, int hi,
+                                                 const unsigned char* tile, bool begun, float m,
+                                                 float M, float l) {
+    return apart_softmax(sc, oc, pid, ks, vlog, shift, qf, lo, hi, tile, begun, m, M, l);
+  }
+
   // The unit's NaN marks, if any, are used up: every row's thread sees the same
   // flag and meets the others before and after they are cleared (two phases of
   // a barrier of 256, where a unit of one half arrives for both).
@@ -637,8 +758,9 @@ struct Softmax {
     q8::MergeMeta* mm = reinterpret_cast<q8::MergeMeta*>(a.meta);
     int tiles = 0, units = 0;
     int others = 0, splits = 0;  // half 0: units that half 1 had a part in; split ones
+    int kv0 = 0;                 // the block's K and V tiles before the unit's
     Walk<SPLIT> w;
-    for (w.start(a, pl, X0, X1); !w.done(); w.next(a, pl)) {
+    for (w.start(a, pl, X0, X1); !w.done(); kv0 += 2 * w.n, w.next(a, pl)) {
       const Unit& u = w.u;
       // (a unit begins when both halves have ended the one before, so that the
       // converters, two units ahead at most, never reach a half's marks in use)
@@ -673,17 +795,47 @@ struct Softmax {
       const int chunks = w.n, h = w.at.h;
       int key0 = w.key0(split ? t : 0);
       bool begun = false;
+      int low = kFar, high = -kFar;  // log2 of the value scales so far
       Pages pg{page_of(a, u, key0, lane, shift), 0.f, 0.f, 0.f};
       pg.scales(a, h);
+      // A chunk's V, for the weights of scales far apart. (Its tile waits for
+      // nothing that waits for this softmax: the tile before it in the ring is K's,
+      // or a V of which the products were issued ahead of these scores.)
+      auto values = [&](int kv) {
+        wait(&B.full[kv % kRing], kv / kRing, abort, a.err);
+        return sm.kv[kv % kRing];
+      };
+      auto take = [&](const Sums& now) {
+        m = now.m;
+        M = now.M;
+        l = now.l;
+      };
 #pragma unroll 1
       for (int i = split ? t : 0; i < chunks; i += step, key0 += step * CK) {
         Pages next{page_of(a, u, key0 + step * CK, lane, shift), 0.f, 0.f, 0.f};
+        auto leave = [&] {  // P is written
+          tc::st_wait();
+          tc::fence_before_sync();
+          ptx::mbar_arrive(&B.p_full[t]);
+          pg = next;
+          begun = true;
+        };
         pg.lv = __log2f(pg.vs);
         const bool mine = lane < CK >> shift;
-        const bool masked = __any_sync(
-            0xffffffffu, (mine && pg.pid < 0) || key0 < lo || key0 + CK > hi);
-        const int least = __reduce_min_sync(
-            0xffffffffu, mine && pg.pid >= 0 ? __float2int_rd(pg.lv) : INT_MAX);
+        const bool edge = (mine && pg.pid < 0) || key0 < lo || key0 + CK > hi;
+        const bool there = mine && pg.pid >= 0;
+        const int level = __float2int_rd(pg.lv);
+        // keys that some row does not see; or, rarely after a unit's first chunk,
+        // scales beyond those before, or the smallest ones
+        bool masked = __any_sync(0xffffffffu, edge || (there && (level < low || level > high)));
+        bool small = false;
+        if (masked) {
+          const bool tiny = level <= (int)q8::kSmall;
+          masked = __any_sync(0xffffffffu, edge);
+          small = __any_sync(0xffffffffu, there && tiny);
+          low = min(low, (int)__reduce_min_sync(0xffffffffu, there && !tiny ? level : kFar));
+          high = max(high, (int)__reduce_max_sync(0xffffffffu, there ? level : -kFar));
+        }
         float c[4], lv[4];  // of 32 scores each
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -693,6 +845,17 @@ struct Softmax {
         wait(&B.s_full[t], tiles++, abort, a.err);
         tc::fence_after_sync();
         const uint32_t sc = tl + s_col(t);
+        const bool far = high - low > (int)q8::kSpread;
+        const int kv = kv0 + 2 * i + (split && i < chunks - 1 ? 2 : 1);  // the chunk's V tile
+        // (a call here: inline, here or below, the split kernel's chunks take 4 to 9 %
+        // longer; the other's take 3 % longer with it, and 1 % less as below)
+        if (SPLIT && __builtin_expect(far, 0)) {
+          next.scales(a, h);
+          take(apart_call(sc, tl + o_col(t), pg.pid, pg.ks, pg.lv, shift, qf, lo - key0, hi - key0,
+                          values(kv), begun, m, M, l));
+          leave();
+          continue;
+        }
         float top = m, ref = M;
         uint32_t z0[32], z1[32];
         if (!masked) {
@@ -728,6 +891,12 @@ struct Softmax {
           }
         }
         next.scales(a, h);  // on their way during the exponentials
+        if (!SPLIT && __builtin_expect(far, 0)) {
+          take(apart_softmax(sc, tl + o_col(t), pg.pid, pg.ks, pg.lv, shift, qf, lo - key0,
+                             hi - key0, values(kv), begun, m, M, l));
+          leave();
+          continue;
+        }
         const float base = top == -INFINITY ? 0.f : top;
         l *= ptx::ex2(m - base);
         m = top;
@@ -748,8 +917,9 @@ struct Softmax {
           }
         }
         const float oref = M == -INFINITY ? 0.f : M;
-        const bool apart = __any_sync(
-            0xffffffffu, fabsf(base) > 4194304.f || !(base - oref + (float)least > -60.f));
+        // (M is at most the maximum's with the largest scale: p * vscale vanishes
+        // before p does beside the smallest scales only)
+        const bool apart = __any_sync(0xffffffffu, small || fabsf(base) > 4194304.f);
         float sum = 0.f;
         if (!masked && !apart) {
 #pragma unroll
@@ -790,11 +960,7 @@ struct Softmax {
           }
         }
         l += sum;
-        tc::st_wait();
-        tc::fence_before_sync();
-        ptx::mbar_arrive(&B.p_full[t]);
-        pg = next;
-        begun = true;
+        leave();
       }
 
       // ---- epilogue ----

@@ -679,6 +679,120 @@ def test_prefill_nan_values_in_many_short_sequences():
         assert torch.equal(out[~want.cuda()], base[~want.cuda()])
 
 
+# ---- value scales that are none of a query's own ------------------------------------
+
+def outlier_cache(p, lens, seed, at, ratio, held=True):
+    """random_cache with scales alike, but for the page of sequence 0's token `at`: its
+    value scale covers values `ratio` times the others', its codes are what is left of
+    the values under it. That token has the largest code everywhere, unless it was
+    written over since (held False: the scale stays)."""
+    cache = random_cache(p, lens, seed, extra=0, spread=0.0)
+    pid, slot = int(cache.page_table[0, at // p.sel_block]), at % p.sel_block
+    codes = (cache.v_pages[pid].float() / ratio).to(torch.float8_e4m3fn).view(torch.uint8)
+    codes[:, slot] = 0x7e if held else 0
+    cache.v_pages.view(torch.uint8)[pid] = codes
+    cache.v_scale[pid] *= ratio
+    return cache
+
+
+OUTLIERS = ((BF16, 128, 64), (BF16, 128, 32), (BF16, 64, 16), (F32, 64, 16), (F32, 128, 128))
+
+
+@pytest.mark.parametrize("dt,d,page", OUTLIERS, ids=str)
+@pytest.mark.parametrize("ratio", (2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100))
+def test_decode_unseen_outlier_values(dt, d, page, ratio):
+    """A value that a query does not see, in a page of which it sees other tokens, takes
+    nothing from the query's sums, however large: a token before the window, one
+    written over since, and one behind the sequence's end."""
+    p = nsa.params(1, 1000, 16, 1, d, sel_block=page, dtype=dt, window=501)
+    q = torch.randn(1, 16, d, generator=gen(91)).to(dt).cuda()
+    lens = i32([1000])
+    first = 1000 - 501
+    for at, held, keys in (((first // page) * page, True, "window"), (999, False, "all"),
+                           (5, False, "all"), (700, False, "window")):
+        cache = outlier_cache(p, [1000], 92, at, ratio, held)
+        got = nsa.nsa_decode_q8(p, q, cache, lens, keys=keys)
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, lens, None, keys)
+    lens = i32([990])  # tokens 990 .. 999 were drafts, refused since
+    cache = outlier_cache(p, [1000], 92, 990 + 5, ratio)
+    got = nsa.nsa_decode_q8(p, q, cache, lens)
+    nsa.nsa_check()
+    check_attention(got, p, q, cache, lens)
+    # a listed block whose scale is none of its codes', before and behind others
+    p = nsa.params(1, 1000, 16, 1, d, sel_block=page, dtype=dt, top_n=5)
+    cache = outlier_cache(p, [1000], 92, 3 * page, ratio, False)
+    for sel in ([3, 0, 1, -1, 6], [0, 1, 6, 2, 3]):
+        got = nsa.nsa_decode_q8(p, q, cache, i32([1000]), keys="blocks", sel_idx=i32([[sel]]))
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, i32([1000]), None, "blocks", torch.tensor([[sel]]))
+
+
+@pytest.mark.parametrize("dt,d,page", OUTLIERS, ids=str)
+@pytest.mark.parametrize("ratio", (2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100))
+def test_prefill_unseen_outlier_values(dt, d, page, ratio):
+    """The same for chunks: queries before the outlier's token, and those whose window
+    has left it, keep their sums; the others have its value."""
+    p = nsa.params(1, 700, 16, 1, d, sel_block=page, dtype=dt, window=130)
+    n = 300
+    q = torch.randn(n, 16, d, generator=gen(93)).to(dt).cuda()
+    lens, cu = i32([700]), i32([0, n])
+    for at, held in ((640, True), (699, True), (405, True), (500, False)):
+        cache = outlier_cache(p, [700], 94, at, ratio, held)
+        for keys in ("all", "window"):
+            got = nsa.nsa_prefill_q8(p, q, cache, lens, cu, keys=keys)
+            nsa.nsa_check()
+            check_attention(got, p, q, cache, lens, cu.cpu(), keys)
+
+
+def test_prefill_drafts_unseen_outlier_values():
+    """Few queries a sequence over many keys, where both tile halves share the keys."""
+    B, new = 20, 4
+    lens = [600 + 37 * b for b in range(B)]
+    p = nsa.params(B, 1400, 16, 1, 128, sel_block=64)
+    q = torch.randn(B * new, 16, 128, generator=gen(95)).to(BF16).cuda()
+    cu = i32([new * b for b in range(B + 1)])
+    for ratio in (2.0 ** 24, 2.0 ** 60):
+        cache = random_cache(p, lens, 96, extra=0, spread=0.0)
+        codes, table = cache.v_pages.view(torch.uint8), cache.page_table.cpu()
+        for b in range(B):  # some page's scale is that of a token written over since,
+            pid = int(table[b, b % 9])
+            codes[pid] = 0
+            cache.v_scale[pid] *= ratio
+            pid = int(table[b, (lens[b] - 1) // 64])  # or of the last draft
+            few = (cache.v_pages[pid].float() / ratio).to(torch.float8_e4m3fn).view(torch.uint8)
+            few[:, (lens[b] - 1) % 64] = 0x7e
+            codes[pid] = few
+            cache.v_scale[pid] *= ratio
+        got = nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu)
+        nsa.nsa_check()
+        check_attention(got, p, q, cache, i32(lens), cu.cpu())
+
+
+@pytest.mark.parametrize("dt,d,page", OUTLIERS, ids=str)
+def test_outlier_in_one_channel(dt, d, page):
+    """A value that is seen, far above the others in one channel: the other channels
+    have its key's weight's share, and at most 2^-33 of the largest product of a weight
+    and a value for each key besides (a weight's last place beside that product)."""
+    p = nsa.params(1, 700, 16, 1, d, sel_block=page, dtype=dt)
+    n = 40
+    q = torch.randn(n, 16, d, generator=gen(97)).to(dt).cuda()
+    lens, cu = i32([700]), i32([0, n])
+    for ratio in (2.0 ** 6, 2.0 ** 12, 2.0 ** 20):
+        cache = outlier_cache(p, [700], 98, 300, ratio)
+        pid = int(cache.page_table[0, 300 // page])
+        cache.v_pages.view(torch.uint8)[pid, :, 300 % page, 1:] = 0
+        got = nsa.nsa_prefill_q8(p, q, cache, lens, cu)
+        nsa.nsa_check()
+        want, wlse, A, B = ref.attend(q, cache.k_pages, cache.v_pages, cache.k_scale,
+                                      cache.v_scale, cache.page_table, lens, page, cu.cpu())
+        t_out, t_lse = ref.bounds(want, wlse, A, B, dt, 700)
+        t_out = t_out + 700 * 2.0 ** -33 * A.amax(-1, keepdim=True)
+        err = (got[0].double().cpu() - want).abs()
+        assert (err <= t_out).all(), float((err / t_out).max())
+        assert ((got[1].double().cpu() - wlse).abs() <= t_lse).all()
+
+
 # ---- together -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dt", (BF16, F32))
