@@ -62,7 +62,9 @@ constexpr int kUnitChunks = 4 * kWarps;  // most chunks of a unit that one block
 constexpr int SLOTS = 3;     // of a warp's ring
 constexpr int kSmemTiles = 1024;  // tiles whose prefix a block computes itself
 constexpr int kFar = 1 << 20;     // beyond every scale's exponent
-constexpr int kAbsent = INT_MAX / 2;  // first key of an absent page: past every row
+// First key of an absent page: past every row (of a sequence of up to 2^30 tokens),
+// its last still an int.
+constexpr int kAbsent = INT_MAX - CK;
 
 template <int D>
 struct Geo {
@@ -220,7 +222,7 @@ struct Feeder {
   // The pages of the chunk at the place.
   __device__ __forceinline__ void look(const Q8AttendArgs& a, ChunkMeta<PP>* meta, int lane) {
     const int ch = at.c + (a.keys == q8::KEYS_BLOCKS ? 0 : u.lo / CK);
-    const int shift = __ffs(a.page) - 1;  // (a call has fewer than 2^30 tokens or listed keys)
+    const int shift = __ffs(a.page) - 1;  // (a sequence or a list has up to 2^30 keys)
     const int e = (ch * CK) >> shift;
     coff = PP == 1 ? ch * CK & (a.page - 1) : 0;
     if (e + PP > gbase + 32 || e < gbase) pages(a, e, lane);

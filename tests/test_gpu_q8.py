@@ -391,6 +391,46 @@ def test_decode_far_positions():
     check_attention(got, p, q, cache, i32([L]), keys="window")
 
 
+@pytest.mark.parametrize("dt,d,page", ((BF16, 128, 64), (F32, 64, 16), (BF16, 64, 128)), ids=str)
+def test_longest_sequence(dt, d, page):
+    """2^30 tokens, on few pages that repeat: listed blocks, the last among them, beside
+    absent ones and one whose number is no page; and a window at the end."""
+    T, n = 1 << 30, (1 << 30) // page
+    small = random_cache(nsa.params(1, 4 * page, 4, 1, d, sel_block=page, dtype=dt), [4 * page], 110)
+    order = small.page_table[0].cpu()
+    table = order.repeat(n // 4)[None].contiguous()
+    table[0, 7] = -5
+    far = nsa.Q8Cache(small.k_pages, small.v_pages, small.k_scale, small.v_scale, table.cuda())
+    q = torch.randn(1, 4, d, generator=gen(111)).to(dt).cuda()
+
+    def near(blocks):
+        t = table[:, blocks].to(torch.int32).contiguous().cuda()
+        return nsa.Q8Cache(small.k_pages, small.v_pages, small.k_scale, small.v_scale, t)
+
+    for sel in ([n - 1, -1, -1, -1, -1, -1], [-1, 5, n - 1, n, -7, n - 3], [-1, 2, -1, -1, 7, -1]):
+        p = nsa.params(1, T, 4, 1, d, sel_block=page, dtype=dt, top_n=6)
+        got = nsa.nsa_decode_q8(p, q, far, i32([T]), keys="blocks", sel_idx=i32([[sel]]))
+        if 7 in sel:
+            with pytest.raises(nsa.NsaError, match="page"):
+                nsa.nsa_check()
+        nsa.nsa_check()
+        live = [b for b in sel if 0 <= b < n and b != 7]
+        p = nsa.params(1, len(live) * page, 4, 1, d, sel_block=page, dtype=dt)
+        check_attention(got, p, q, near(live), i32([len(live) * page]))
+    p = nsa.params(1, T, 1, 1, d, sel_block=page, dtype=dt, window=2 * page + 3)
+    q = torch.randn(40, 1, d, generator=gen(112)).to(dt).cuda()
+    got = nsa.nsa_prefill_q8(p, q, far, i32([T]), i32([0, 40]), keys="window")
+    nsa.nsa_check()
+    blocks = list(range(n - 2 - -(-48 // page), n))
+    pn = nsa.params(1, len(blocks) * page, 1, 1, d, sel_block=page, dtype=dt, window=2 * page + 3)
+    assert len(blocks) * page >= 2 * page + 3 + 40
+    check_attention(got, pn, q, near(blocks), i32([len(blocks) * page]), i32([0, 40]).cpu(), "window")
+    last = q[-1:].contiguous()
+    got = nsa.nsa_decode_q8(p, last, far, i32([T]), keys="window")
+    nsa.nsa_check()
+    check_attention(got, pn, last, near(blocks), i32([len(blocks) * page]), None, "window")
+
+
 def test_pool_beyond_32_bit_offsets():
     """Pages whose bytes lie past 2^31 of the pool: appended and attended to."""
     Hkv, page, d = 4, 64, 128

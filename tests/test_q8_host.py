@@ -73,6 +73,15 @@ def test_cache_and_parameters_are_checked(call):
         assert call(bad, **({} if call is append else {"nbytes": 0})) in (1, 2)
 
 
+def test_longest_sequence():
+    """T up to 2^30 is taken, and no more (positions, and what lies past them, are ints)."""
+    n = ctypes.c_size_t()
+    for T, want in ((1 << 30, 0), ((1 << 30) + 1, 2)):
+        p = nsa.params(1, T, 1, 1, 64)
+        for op in (nsa.OP_DECODE_Q8, nsa.OP_PREFILL_Q8):
+            assert L.nsa_workspace_size(ctypes.byref(p), op, ctypes.byref(n)) == want
+
+
 def test_append_refusals():
     assert append(P, k=None) == 1 and append(P, v=None) == 1 and append(P, pos=None) == 1
     assert append(P, N=3) == 1 and "cu_new" in detail()  # one token per sequence: N == B
