@@ -7,6 +7,10 @@ the import fails loudly -- there is no fallback.
 
 Names mirror the C ABI in ``include/nsa.h``: ``nsa_compress_kv``,
 ``nsa_prefill``, ``nsa_decode``, ``moba_prefill``, ``nsa_check``.
+
+A call given ``stream`` runs as it would with that stream current: outputs and
+workspaces that it makes are of that stream's memory, and the caller orders the
+stream with those that its inputs come from and its outputs go to.
 """
 import ctypes
 import os
@@ -197,9 +201,25 @@ def workspace_size(p, op):
     return n.value
 
 
-def workspace(p, op, device="cuda"):
+def _empty(stream, *shape, **kw):
+    """torch.empty for a call on `stream` (None: the current one). The memory is that
+    stream's: what was in it before is done when the call starts, and what a call made
+    for itself is free again when the call is done."""
+    if stream is None:
+        return torch.empty(*shape, **kw)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, **kw)
+
+
+def _empty_like(stream, t):
+    return torch.empty_like(t) if stream is None else _empty(stream, t.shape, dtype=t.dtype,
+                                                             device=t.device)
+
+
+def workspace(p, op, device="cuda", stream=None):
+    """A workspace for op, of the memory of `stream` (None: the current one)."""
     n = workspace_size(p, op)
-    return torch.empty(max(n, 1), dtype=torch.uint8, device=device) if n else None
+    return _empty(stream, max(n, 1), dtype=torch.uint8, device=device) if n else None
 
 
 def nsa_compress_kv(p, k, v, w_cmp, k_cmp=None, v_cmp=None, stream=None):
@@ -211,9 +231,9 @@ def nsa_compress_kv(p, k, v, w_cmp, k_cmp=None, v_cmp=None, stream=None):
     Nc = num_cmp_blocks(p.T, p.cmp_block, p.cmp_stride)
     shape = (p.B, Nc, p.Hkv, p.d)
     if k_cmp is None:
-        k_cmp = torch.empty(shape, dtype=dt, device=dev)
+        k_cmp = _empty(stream, shape, dtype=dt, device=dev)
     if v_cmp is None:
-        v_cmp = torch.empty(shape, dtype=dt, device=dev)
+        v_cmp = _empty(stream, shape, dtype=dt, device=dev)
     _dev(k_cmp, "k_cmp", dt, dev)
     _dev(v_cmp, "v_cmp", dt, dev)
     with _on(dev):
@@ -231,13 +251,13 @@ def nsa_prefill(p, q, k, v, k_cmp, v_cmp, w_gate=None, out=None, sel_idx=None, w
         _dev(t, nm, dt, dev)
     _dev(w_gate, "w_gate", torch.float32, dev)
     if out is None:
-        out = torch.empty(p.B, p.T, p.Hq, p.d, dtype=dt, device=dev)
+        out = _empty(stream, p.B, p.T, p.Hq, p.d, dtype=dt, device=dev)
     if sel_idx is None and want_sel:
-        sel_idx = torch.empty(p.B, p.T, p.Hkv, p.top_n, dtype=torch.int32, device=dev)
+        sel_idx = _empty(stream, p.B, p.T, p.Hkv, p.top_n, dtype=torch.int32, device=dev)
     _dev(out, "out", dt, dev)
     _dev(sel_idx, "sel_idx", torch.int32, dev)
     if ws is None:
-        ws = workspace(p, OP_PREFILL, dev)
+        ws = workspace(p, OP_PREFILL, dev, stream)
     _dev(ws, "ws", None, dev)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     with _on(dev):
@@ -259,13 +279,13 @@ def nsa_prefill_backward(p, q, k, v, k_cmp, v_cmp, w_cmp, w_gate, sel_idx, dout,
     _dev(w_gate, "w_gate", torch.float32, dev)
     _dev(sel_idx, "sel_idx", torch.int32, dev)
     f32 = dict(dtype=torch.float32, device=dev)
-    dq = torch.empty(p.B, p.T, p.Hq, p.d, **f32)
-    dk = torch.empty(p.B, p.T, p.Hkv, p.d, **f32)
-    dv = torch.empty(p.B, p.T, p.Hkv, p.d, **f32)
-    dw_cmp = torch.empty(p.cmp_block, **f32)
-    dw_gate = torch.empty(p.d, 3, **f32)
+    dq = _empty(stream, p.B, p.T, p.Hq, p.d, **f32)
+    dk = _empty(stream, p.B, p.T, p.Hkv, p.d, **f32)
+    dv = _empty(stream, p.B, p.T, p.Hkv, p.d, **f32)
+    dw_cmp = _empty(stream, p.cmp_block, **f32)
+    dw_gate = _empty(stream, p.d, 3, **f32)
     if ws is None:
-        ws = workspace(p, OP_PREFILL_BACKWARD, dev)
+        ws = workspace(p, OP_PREFILL_BACKWARD, dev, stream)
     _dev(ws, "ws", None, dev)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     with _on(dev):
@@ -277,7 +297,7 @@ def nsa_prefill_backward(p, q, k, v, k_cmp, v_cmp, w_cmp, w_gate, sel_idx, dout,
 
 
 def _decode_args(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate, out, sel_idx,
-                 want_sel):
+                 want_sel, stream):
     """Checks of the decode arguments (one device for all); allocates the
     outputs that are not given."""
     dt = p.torch_dtype
@@ -289,9 +309,9 @@ def _decode_args(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate, out, se
     _dev(seq_lens, "seq_lens", torch.int32, dev)
     _dev(w_gate, "w_gate", torch.float32, dev)
     if out is None:
-        out = torch.empty(p.B, p.Hq, p.d, dtype=dt, device=dev)
+        out = _empty(stream, p.B, p.Hq, p.d, dtype=dt, device=dev)
     if sel_idx is None and want_sel:
-        sel_idx = torch.empty(p.B, p.Hkv, p.top_n, dtype=torch.int32, device=dev)
+        sel_idx = _empty(stream, p.B, p.Hkv, p.top_n, dtype=torch.int32, device=dev)
     _dev(out, "out", dt, dev)
     _dev(sel_idx, "sel_idx", torch.int32, dev)
     return out, sel_idx
@@ -300,10 +320,10 @@ def _decode_args(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate, out, se
 def nsa_decode(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate=None, out=None,
                sel_idx=None, ws=None, stream=None, want_sel=True):
     out, sel_idx = _decode_args(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate, out,
-                                sel_idx, want_sel)
+                                sel_idx, want_sel, stream)
     dev = q.device
     if ws is None:
-        ws = workspace(p, OP_DECODE, dev)
+        ws = workspace(p, OP_DECODE, dev, stream)
     _dev(ws, "ws", None, dev)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     with _on(dev):
@@ -320,7 +340,7 @@ def nsa_decode_noalloc(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate=No
     calls must not overlap on the GPU). The C call allocates nothing; this
     wrapper allocates `out` / `sel_idx` only when they are not given."""
     out, sel_idx = _decode_args(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate, out,
-                                sel_idx, want_sel)
+                                sel_idx, want_sel, stream)
     dev = q.device
     # the device current during the call selects which GPU's static scratch is used
     with _on(dev):
@@ -356,7 +376,7 @@ def nsa_block_bounds(p, k_cache, seq_lens, k_bounds=None, stream=None):
     _dev(seq_lens, "seq_lens", torch.int32, dev)
     nblk = -(-p.T // p.sel_block)
     if k_bounds is None:
-        k_bounds = torch.empty(p.B, nblk, p.Hkv, 2, p.d, dtype=dt, device=dev)
+        k_bounds = _empty(stream, p.B, nblk, p.Hkv, 2, p.d, dtype=dt, device=dev)
     _dev(k_bounds, "k_bounds", dt, dev)
     with _on(dev):
         _raise(LIB.nsa_block_bounds(ctypes.byref(p), _ptr(k_cache), _ptr(seq_lens), _ptr(k_bounds),
@@ -381,11 +401,11 @@ def nsa_decode_quest(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, k_bounds, w
     """nsa_decode ranking blocks by the Quest-style bound from k_bounds
     (p.sel_mode must be 1)."""
     out, sel_idx = _decode_args(p, q, k_cache, v_cache, seq_lens, k_cmp, v_cmp, w_gate, out,
-                                sel_idx, want_sel)
+                                sel_idx, want_sel, stream)
     dev = q.device
     _dev(k_bounds, "k_bounds", p.torch_dtype, dev)
     if ws is None:
-        ws = workspace(p, OP_DECODE, dev)
+        ws = workspace(p, OP_DECODE, dev, stream)
     _dev(ws, "ws", None, dev)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     with _on(dev):
@@ -403,13 +423,13 @@ def moba_prefill(p, q, k, v, out=None, sel_idx=None, ws=None, stream=None, want_
     _dev(k, "k", dt, dev)
     _dev(v, "v", dt, dev)
     if out is None:
-        out = torch.empty(p.B, p.T, p.Hq, p.d, dtype=dt, device=dev)
+        out = _empty(stream, p.B, p.T, p.Hq, p.d, dtype=dt, device=dev)
     if sel_idx is None and want_sel:
-        sel_idx = torch.empty(p.B, p.T, p.Hq, p.top_n, dtype=torch.int32, device=dev)
+        sel_idx = _empty(stream, p.B, p.T, p.Hq, p.top_n, dtype=torch.int32, device=dev)
     _dev(out, "out", dt, dev)
     _dev(sel_idx, "sel_idx", torch.int32, dev)
     if ws is None:
-        ws = workspace(p, OP_MOBA_PREFILL, dev)
+        ws = workspace(p, OP_MOBA_PREFILL, dev, stream)
     _dev(ws, "ws", None, dev)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     with _on(dev):
@@ -523,15 +543,15 @@ def nsa_append_q8(p, k_new, v_new, pos, cache, cu_new=None, q=None, rope=None, r
     _is(v_new, "v_new", dt, dev, kv)
     _is(q, "q", dt, dev, qs)
     if q is not None and q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _empty_like(stream, q)
     else:
         _is(q_out, "q_out", dt, dev, qs)
     if want_kv and k_out is None:
-        k_out = torch.empty_like(k_new)
+        k_out = _empty_like(stream, k_new)
     elif k_out is not None:
         _is(k_out, "k_out", dt, dev, kv)
     if want_kv and v_out is None:
-        v_out = torch.empty_like(k_new)
+        v_out = _empty_like(stream, k_new)
     elif v_out is not None:
         _is(v_out, "v_out", dt, dev, kv)
     _is(pos, "pos", torch.int32, dev, (p.B,))
@@ -553,7 +573,7 @@ def nsa_append_q8(p, k_new, v_new, pos, cache, cu_new=None, q=None, rope=None, r
     return q_out, k_out, v_out
 
 
-def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op):
+def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op, stream):
     """Checks of the attention arguments; allocates what is not given."""
     dt, dev = p.torch_dtype, cache.device
     cache._fits(p)
@@ -562,16 +582,16 @@ def _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws, op):
     shape = (N, p.Hq, p.d)
     _is(q, "q", dt, dev, shape)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     else:
         _is(out, "out", dt, dev, shape)
     if lse is None:
-        lse = cache.k_scale.new_empty(shape[:2])
+        lse = _empty(stream, shape[:2], dtype=torch.float32, device=dev)
     else:
         _is(lse, "lse", torch.float32, dev, shape[:2])
     _is(seq_lens, "seq_lens", torch.int32, dev, (p.B,))
     if ws is None:
-        ws = workspace(p, op, dev)
+        ws = workspace(p, op, dev, stream)
     elif ws.get_device() != dev.index or not ws.is_contiguous():
         _dev(ws, "ws", None, dev)
     return out, lse, ws, ws.nbytes
@@ -583,7 +603,7 @@ def nsa_decode_q8(p, q, cache, seq_lens, keys="all", sel_idx=None, out=None, lse
     8-bit cache: all keys, the last p.window, or those in the blocks sel_idx
     [B, Hkv, p.top_n]. Returns (out, lse [B, Hq] fp32)."""
     out, lse, ws, nbytes = _attend_q8_args(p, q, p.B, cache, seq_lens, keys, out, lse, ws,
-                                           OP_DECODE_Q8)
+                                           OP_DECODE_Q8, stream)
     dev = cache.device
     if sel_idx is not None:
         _is(sel_idx, "sel_idx", torch.int32, dev, (p.B, p.Hkv, p.top_n))
@@ -599,7 +619,7 @@ def nsa_prefill_q8(p, q, cache, seq_lens, cu_q=None, keys="all", out=None, lse=N
     all earlier keys or the last p.window. Returns (out, lse [N, Hq] fp32)."""
     N = q.shape[0]
     out, lse, ws, nbytes = _attend_q8_args(p, q, N, cache, seq_lens, keys, out, lse, ws,
-                                           OP_PREFILL_Q8)
+                                           OP_PREFILL_Q8, stream)
     dev = cache.device
     _is(cu_q, "cu_q", torch.int32, dev, (p.B + 1,))
     _call(LIB.nsa_prefill_q8, dev, stream, ctypes.byref(p), cache.ref, _addr(q), N, _addr(cu_q),

@@ -318,3 +318,60 @@ def test_prefill_top_p_stops_before_n():
     nsa.nsa_check()
     counts = (sel[0, 1100:, 0] >= 0).sum(-1)
     assert int(counts.min()) < w["top_n"] and int(counts.max()) >= 2
+
+
+def _owner(t):
+    """The stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= at < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_a_given_stream_owns_what_a_call_makes(monkeypatch):
+    """Outputs and workspaces that a call makes for a given stream lie in that stream's
+    memory, the workspace too, which is free again on return while kernels use it."""
+    from dynamic_block_sparse_nsa_b200 import nsa
+    made, empty = [], torch.empty
+
+    def spy(*a, **kw):
+        made.append(empty(*a, **kw))
+        return made[-1]
+
+    side = torch.cuda.Stream()
+    w = inputs.workload("nsa_prefill_bf16_t8192", T=300, Hq=16, Hkv=1)
+    x = {n: t.cuda() for n, t in inputs.make_prefill(w, seed=5).items()}
+    p = gc.nsa_params_for(w)
+    kc, vc = nsa.nsa_compress_kv(p, x["k"], x["v"], x["w_cmp"])
+    out, sel = nsa.nsa_prefill(p, x["q"], x["k"], x["v"], kc, vc, x["w_gate"])
+    lens = torch.full((p.B,), 300, dtype=torch.int32, device="cuda")
+    q1 = x["q"][:, -1].contiguous()
+    bounds = nsa.nsa_block_bounds(p, x["k"], lens)
+    quest = gc.nsa_params_for(w)
+    quest.sel_mode = 1
+    wm = inputs.workload("moba_prefill_bf16_t131072", T=512, Hq=2, Hkv=2, block=256, top_k=2)
+    xm = {n: t.cuda() for n, t in inputs.make_prefill(wm, seed=6).items()}
+    pm = gc.moba_params_for(wm)
+    calls = {
+        "compress": lambda s: nsa.nsa_compress_kv(p, x["k"], x["v"], x["w_cmp"], stream=s),
+        "prefill": lambda s: nsa.nsa_prefill(p, x["q"], x["k"], x["v"], kc, vc, x["w_gate"], stream=s),
+        "backward": lambda s: nsa.nsa_prefill_backward(p, x["q"], x["k"], x["v"], kc, vc, x["w_cmp"],
+                                                       x["w_gate"], sel, out, stream=s),
+        "decode": lambda s: nsa.nsa_decode(p, q1, x["k"], x["v"], lens, kc, vc, x["w_gate"], stream=s),
+        "bounds": lambda s: (nsa.nsa_block_bounds(p, x["k"], lens, stream=s),),
+        "quest": lambda s: nsa.nsa_decode_quest(quest, q1, x["k"], x["v"], lens, kc, vc, bounds,
+                                                x["w_gate"], stream=s),
+        "moba": lambda s: nsa.moba_prefill(pm, xm["q"], xm["k"], xm["v"], stream=s),
+    }
+    for name, call in calls.items():
+        want = call(None)
+        torch.cuda.synchronize()
+        made.clear()
+        monkeypatch.setattr(torch, "empty", spy)
+        got = call(side)
+        monkeypatch.setattr(torch, "empty", empty)
+        torch.cuda.synchronize()
+        assert made and all(_owner(t) == side.cuda_stream for t in made), name
+        for a, b in zip(got, want):
+            torch.testing.assert_close(a, b, rtol=1e-5, atol=1e-5, msg=name)
+    nsa.nsa_check()

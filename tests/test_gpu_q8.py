@@ -936,6 +936,42 @@ def test_two_streams_with_their_own_workspaces():
     nsa.nsa_check()
 
 
+def test_a_given_stream_owns_what_a_call_makes(monkeypatch):
+    """As tests/test_gpu_nsa.py's: outputs and workspaces made for a call on a stream."""
+    from tests.test_gpu_nsa import _owner
+    made, empty = [], torch.empty
+
+    def spy(*a, **kw):
+        made.append(empty(*a, **kw))
+        return made[-1]
+
+    p = nsa.params(2, 256, 16, 1, 128, sel_block=64)
+    q = torch.randn(6, 16, 128, generator=gen(120)).to(BF16).cuda()
+    k, v = (torch.randn(6, 1, 128, generator=gen(121 + i)).to(BF16).cuda() for i in range(2))
+    lens, cu, rope = i32([200, 99]), i32([0, 4, 6]), nsa.rope_table(256, 128)
+    first = q[:2].contiguous()
+    side = torch.cuda.Stream()
+    calls = {
+        "append": lambda c, s: nsa.nsa_append_q8(p, k, v, i32([196, 97]), c, cu_new=cu, q=q, rope=rope,
+                                                 want_kv=True, stream=s),
+        "decode": lambda c, s: nsa.nsa_decode_q8(p, first, c, lens, stream=s),
+        "prefill": lambda c, s: nsa.nsa_prefill_q8(p, q, c, lens, cu, stream=s),
+    }
+    for name, call in calls.items():
+        want = call(random_cache(p, [200, 99], 122), None)
+        cache = random_cache(p, [200, 99], 122)
+        torch.cuda.synchronize()
+        made.clear()
+        monkeypatch.setattr(torch, "empty", spy)
+        got = call(cache, side)
+        monkeypatch.setattr(torch, "empty", empty)
+        torch.cuda.synchronize()
+        assert len(made) == 3 and all(_owner(t) == side.cuda_stream for t in made), name
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), name
+    nsa.nsa_check()
+
+
 def test_wrapper_refusals():
     p = nsa.params(2, 100, 4, 2, 64, sel_block=32)
     cache = random_cache(p, [100, 50], 70)
