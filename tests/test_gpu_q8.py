@@ -719,6 +719,164 @@ def test_prefill_nan_values_in_many_short_sequences():
         assert torch.equal(out[~want.cuda()], base[~want.cuda()])
 
 
+def nan_marks(p, cache, lens, new, at, dims):
+    """NaN value codes at positions at[b] of each sequence, component dims[b], in both
+    their tables' pages; the elements [N, Hq, d] of a chunk call that they reach."""
+    G, table = p.Hq // p.Hkv, cache.page_table.cpu()
+    codes = cache.v_pages.view(torch.uint8)
+    want = torch.zeros(sum(new), p.Hq, p.d, dtype=torch.bool)
+    first = 0
+    for b, n in enumerate(new):
+        h = b % p.Hkv
+        codes[int(table[b, at[b] // p.sel_block]), h, at[b] % p.sel_block, dims[b]] = 0x7f
+        sees = max(0, at[b] - (lens[b] - n))  # the first query that sees it
+        want[first + sees:first + n, h * G:(h + 1) * G, dims[b]] = True
+        first += n
+    return want
+
+
+@pytest.mark.parametrize("page", (32, 64, 128))
+def test_prefill_nan_values_of_drafts(page):
+    """Marks of NaN values where both tile halves share a unit's keys: few queries a
+    sequence, warps without rows, several chunks, units cut between blocks."""
+    B = 40
+    new = [(2, 6, 1, 5, 4, 6)[b % 6] for b in range(B)]
+    lens = [300 + 41 * b for b in range(B)]
+    cu = [sum(new[:b]) for b in range(B + 1)]
+    p = nsa.params(B, 2048, 16, 1, 128, sel_block=page)
+    assert 32 * B <= cu[-1] * 16 <= 128 * B
+    cache = random_cache(p, lens, 130)
+    q = torch.randn(cu[-1], 16, 128, generator=gen(131)).to(BF16).cuda()
+    base = nsa.nsa_prefill_q8(p, q, cache, i32(lens), i32(cu))
+    nsa.nsa_check()
+    check_attention(base, p, q, cache, i32(lens), i32(cu).cpu())
+    # among the new tokens, in the chunk before them, and far before them
+    for at in ([lens[b] - 1 - b % new[b] for b in range(B)],
+               [lens[b] - new[b] - 1 - b % 100 for b in range(B)], [7 * b for b in range(B)]):
+        want = nan_marks(p, cache, lens, new, at, [(11 * b) % 128 for b in range(B)])
+        for _ in range(3):
+            out, lse = nsa.nsa_prefill_q8(p, q, cache, i32(lens), i32(cu))
+            nsa.nsa_check()
+            assert torch.equal(torch.isnan(out).cpu(), want)
+            assert torch.equal(out[~want.cuda()], base[0][~want.cuda()]) and torch.equal(lse, base[1])
+        cache = random_cache(p, lens, 130)
+
+
+@pytest.mark.parametrize("keys", ("all", "window"))
+def test_prefill_shared_units_among_others(keys):
+    """Units that the tile halves share between units of two halves of several chunks
+    and units of one chunk, in one call; with NaN values in every sequence's last chunk."""
+    new = [2, 20, 3, 1, 12, 2, 2, 9, 1, 1, 4, 2, 1, 3, 2, 1, 2, 1, 1, 2]
+    lens = [1500, 1400, 100, 9, 777, 2900, 50, 640, 1, 130, 2048, 300, 260, 3, 1023, 64, 513, 128, 2, 2000]
+    B, N = len(new), sum(new)
+    cu = [sum(new[:b]) for b in range(B + 1)]
+    p = nsa.params(B, 3000, 32, 2, 128, sel_block=64, window=600)
+    assert 32 * B <= N * 16 <= 128 * B and max(new) * 16 > 256
+    cache = random_cache(p, lens, 132)
+    q = torch.randn(N, 32, 128, generator=gen(133)).to(BF16).cuda()
+    base = nsa.nsa_prefill_q8(p, q, cache, i32(lens), i32(cu), keys=keys)
+    nsa.nsa_check()
+    check_attention(base, p, q, cache, i32(lens), i32(cu).cpu(), keys)
+    want = nan_marks(p, cache, lens, new, [n - 1 - b % m for b, (n, m) in enumerate(zip(lens, new))],
+                     [(5 * b) % 128 for b in range(B)])
+    for _ in range(3):
+        out, lse = nsa.nsa_prefill_q8(p, q, cache, i32(lens), i32(cu), keys=keys)
+        nsa.nsa_check()
+        assert torch.equal(torch.isnan(out).cpu(), want)
+        assert torch.equal(out[~want.cuda()], base[0][~want.cuda()]) and torch.equal(lse, base[1])
+
+
+@pytest.mark.parametrize("dt", (BF16, F32))
+@pytest.mark.parametrize("B,Hq,Hkv,page,longest", ((3, 40, 2, 64, 700), (1200, 2, 1, 32, 90), (9, 8, 8, 16, 300)))
+def test_prefill_without_offsets_equals_decode(dt, B, Hq, Hkv, page, longest):
+    lens = torch.randint(0, longest + 1, (B,), generator=gen(134)).tolist()
+    for d in (64, 128):
+        p = nsa.params(B, longest, Hq, Hkv, d, sel_block=page, dtype=dt, window=70)
+        cache = random_cache(p, lens, 135)
+        q = torch.randn(B, Hq, d, generator=gen(136)).to(dt).cuda()
+        for keys in ("all", "window"):
+            one = nsa.nsa_decode_q8(p, q, cache, i32(lens), keys=keys)
+            two = nsa.nsa_prefill_q8(p, q, cache, i32(lens), keys=keys)
+            nsa.nsa_check()
+            assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+        check_attention(one, p, q, cache, i32(lens), keys="window")
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,page,N", (
+    (BF16, 64, 4, 64, 2600),   # query rows in a launch of their own; tensor memory
+    (BF16, 16, 1, 32, 24),     # few queries a sequence
+    (BF16, 8, 2, 16, 150),     # not the tensor memory's
+    (F32, 6, 3, 64, 90),
+), ids=str)
+def test_captured_chunks_serve_other_lengths(dt, Hq, Hkv, page, N):
+    """One graph of an append and two attention calls over chunks, replayed with other
+    offsets, lengths and positions in the same tensors: the bits of eager calls."""
+    B, T, d = 4, 3200, 128
+    p = nsa.params(B, T, Hq, Hkv, d, sel_block=page, dtype=dt, window=200)
+    rope = nsa.rope_table(T, d)
+    table = torch.randperm(B * T // page, generator=gen(140)).view(B, -1).to(torch.int32).cuda()
+    g = gen(141)
+
+    def filled():
+        c = nsa.q8_cache(p, B * T // page, table)
+        for t, seed in ((c.k_pages, 142), (c.v_pages, 143)):
+            x = torch.randn(t.shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda")
+            t.copy_((x * 64).to(torch.float8_e4m3fn))
+        c.k_scale.fill_(2.0 ** -6)
+        c.v_scale.fill_(2.0 ** -6)
+        return c
+
+    q, k, v = (torch.randn(N, h, d, generator=g).to(dt).cuda() for h in (Hq, Hkv, Hkv))
+    pos, lens = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    q_rot = torch.empty_like(q)
+    outs = [(torch.empty_like(q), torch.empty(N, Hq, device="cuda")) for _ in range(2)]
+    ws = nsa.workspace(p, nsa.OP_PREFILL_Q8)
+
+    def step(c, qr, o):
+        nsa.nsa_append_q8(p, k, v, pos, c, cu_new=cu, q=q, rope=rope, q_out=qr)
+        for keys, (out, lse) in zip(("all", "window"), o):
+            nsa.nsa_prefill_q8(p, qr, c, lens, cu, keys=keys, out=out, lse=lse, ws=ws)
+
+    def shape(shares, past):
+        new = [int(N * s) for s in shares]
+        cu.copy_(i32([sum(new[:b]) for b in range(B + 1)]))
+        pos.copy_(i32(past))
+        lens.copy_(i32([a + n for a, n in zip(past, new)]))
+
+    cache = filled()
+    shape((0.25, 0.25, 0.25, 0.25), [100, 0, 7, 1900])
+    step(cache, q_rot, outs)  # (loads the kernels)
+    nsa.nsa_check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(cache, q_rot, outs)
+    for shares, past in (((0.25, 0.25, 0.25, 0.25), [100, 0, 7, 1900]), ((0.9, 0.05, 0.0, 0.0), [400, 3000, 5, 0]),
+                         ((0.0, 0.0, 1.0, 0.0), [9, 9, 577, 9]), ((0.4, 0.1, 0.2, 0.3), [0, 0, 0, 0])):
+        shape(shares, past)
+        fresh, other = filled(), torch.full_like(q, 3.0)
+        want = [(torch.full_like(q, 3.0), torch.full((N, Hq), 3.0, device="cuda")) for _ in range(2)]
+        step(fresh, other, want)
+        kept = filled()
+        for a, b in ((cache.k_pages, kept.k_pages), (cache.v_pages, kept.v_pages),
+                     (cache.k_scale, kept.k_scale), (cache.v_scale, kept.v_scale)):
+            a.copy_(b)
+        q_rot.fill_(3.0)
+        for out, lse in outs:
+            out.fill_(3.0)
+            lse.fill_(3.0)
+        graph.replay()
+        nsa.nsa_check()
+        for a, b in ((cache.k_pages, fresh.k_pages), (cache.v_pages, fresh.v_pages)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert torch.equal(cache.k_scale, fresh.k_scale) and torch.equal(cache.v_scale, fresh.v_scale)
+        assert torch.equal(q_rot, other)
+        for a, b in zip(outs, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # ---- value scales that are none of a query's own ------------------------------------
 
 def outlier_cache(p, lens, seed, at, ratio, held=True):
