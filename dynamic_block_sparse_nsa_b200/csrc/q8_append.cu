@@ -129,6 +129,7 @@ __device__ __forceinline__ void put_codes(const float (&x)[16], float s, float i
 // slots then cannot hold becomes NaN.
 __device__ __forceinline__ void recode(uint8_t* page, int bytes, float ratio, int thread,
                                        int threads) {
+  ratio = fminf(ratio, 0x1p100f);  // (more than enough for NaN; 0 * infinity is none of 0's)
 #pragma unroll 4
   for (int at = 16 * thread; at < bytes; at += 16 * threads) {
     uint4 v = *reinterpret_cast<const uint4*>(page + at);

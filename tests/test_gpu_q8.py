@@ -310,6 +310,26 @@ def test_append_reports_bad_positions_pages_and_offsets():
     assert "page" in text and not cache.k_pages.view(torch.uint8).any()
 
 
+@pytest.mark.parametrize("offsets", (False, True))
+def test_append_recodes_zeros_of_any_scale(offsets):
+    """Stale slots of a page begun anew: zeros stay zeros under every scale, and
+    others become NaN where the new one cannot hold them, up to 2^246 below."""
+    p = nsa.params(2, 64, 2, 2, 64, sel_block=32, dtype=F32)
+    for old in (2.0 ** -126, 1.0, 8.0, 2.0 ** 100, 2.0 ** 120):
+        for new in (0.0, 2.0 ** -100, 1.0, 2.0 ** 127):
+            cache = random_cache(p, [0, 0], 160, extra=4)
+            cache.page_table.copy_(i32([[0, 1], [2, 3]]))
+            codes = torch.randint(0, 256, cache.k_pages.shape, generator=gen(161), dtype=torch.uint8)
+            codes[..., ::4] = 0
+            codes[..., 1::4] = 0x80
+            for t in (cache.k_pages, cache.v_pages):
+                t.view(torch.uint8).copy_(codes)
+            cache.k_scale.fill_(old)
+            cache.v_scale.fill_(old)
+            k = torch.full((2, 2, 64), new, device="cuda")
+            check_append(p, cache, k, k, i32([0, 32]), i32([0, 1, 2]) if offsets else None, None, "half")
+
+
 # ---- attention: single tokens ---------------------------------------------------
 
 DECODES = [
