@@ -14,10 +14,11 @@
 // Bound by bytes (each input read once, each output written once) for long
 // calls and by latency for one token per sequence. A (page, head) of K or V is
 // one block's work: its rows stay in registers between the maximum and the
-// codes, so nothing is read from memory twice. Query rows have a kernel of their
-// own ahead of it, which the pages' blocks overlap, or blocks behind the pages'
-// where they are few. With one token per sequence a
-// warp takes a (sequence, head) of K or V instead, and more warps the query rows.
+// codes, and no row is read twice (rows of the rotation table are, by each of the
+// two passes). Query rows have a kernel of their own ahead of it, which the pages'
+// blocks overlap, or blocks behind the pages' where they are few. With one token
+// per sequence a warp takes a (sequence, head) of K or V instead, and more warps
+// the query rows.
 // Measured, 64 query heads on 4 KV heads, d = 128, bf16: 8192 tokens 64 us, 4.9
 // TB/s in and out (loads in flight bound the query rows); 32 sequences of a token
 // each 3.4 us. 11 chunks of up to 701 fp32 tokens (12 heads on 3, d = 64) 13 us.
@@ -63,9 +64,9 @@ __device__ __forceinline__ void turn_of(float (&cs)[16], const Q8AppendArgs& a, 
   }
 }
 
-// Rotates a pair. The products are rounded apart, not fused into the sum: any
-// fp32 evaluation of the formula then gives the same key, and the same code where
-// it lies near the middle of two.
+// Rotates a pair. The products are rounded apart, not fused into the sum: any fp32
+// evaluation that rounds each product then gives the same key, and the same code
+// where it lies near the middle of two (a fused one may not).
 __device__ __forceinline__ void turn_pair(float& u, float& v, float c, float s) {
   const float a = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
   v = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
@@ -438,6 +439,8 @@ cudaError_t launch(const Q8AppendArgs& a, cudaStream_t stream) {
   // tokens 9.4 us against 11.3, and 2 us less on the host; 2000 tokens 16.9 and
   // 17.4; 3000 tokens 29.8 and 27.2, for the pages' registers leave fewer blocks
   // of query rows on an SM).
+  // (An ordinary launch, which all work before it precedes: the pages' kernel, launched
+  // programmatically behind it, reads its inputs without a wait.)
   const bool together = blocks <= kTogether;
   if (!together) {
     TraceScope trace("append_q8_query", stream);

@@ -180,8 +180,10 @@ struct MergeMeta {
   int from, pad;
 };
 
-// Launches so that the grid may be scheduled while its predecessor in the
-// stream drains; every kernel here waits (grid_dep_wait) before it reads.
+// Launches so that the grid may be scheduled while its predecessor in the stream
+// drains. The attention kernels wait (grid_dep_wait) before they read; the append's
+// pages' kernel waits as it ends: its predecessor, an ordinary launch, is the query
+// kernel, of which it reads nothing.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args&&... args) {

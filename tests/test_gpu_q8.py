@@ -310,6 +310,52 @@ def test_append_reports_bad_positions_pages_and_offsets():
     assert "page" in text and not cache.k_pages.view(torch.uint8).any()
 
 
+def turned_fp32(x, table, positions, style):
+    """x fp32 [N, H, d] rotated in fp32, each product and each sum rounded."""
+    t = table[positions]
+    c, s, half = t[:, 0, None], t[:, 1, None], t.shape[-1]
+    i = torch.arange(half, device=x.device)
+    a, b = (i, i + half) if style == "half" else (2 * i, 2 * i + 1)
+    y = x.clone()
+    xa_c, xb_s, xb_c, xa_s = x[..., a] * c, x[..., b] * s, x[..., b] * c, x[..., a] * s
+    y[..., a] = xa_c - xb_s
+    y[..., b] = xb_c + xa_s
+    return y
+
+
+@pytest.mark.parametrize("dt", (BF16, F32))
+@pytest.mark.parametrize("style,d,rot", (("half", 128, 128), ("pairs", 128, 64), ("half", 64, 32), ("pairs", 64, 64)))
+def test_append_rotation_is_that_of_rounded_products(dt, style, d, rot):
+    """Queries, key codes and scales bit for bit, of chunks (with the query rows in the
+    pages' launch and in one of their own) and of one token a sequence."""
+    page, Hq, Hkv = 64, 16, 2
+    for B, n in ((1, 128), (2, 2304), (40, 1)):
+        T = 4000
+        p = nsa.params(B, T, Hq, Hkv, d, sel_block=page, dtype=dt)
+        wide = -(-T // page)
+        cache = nsa.q8_cache(p, B * wide, torch.arange(B * wide, dtype=torch.int32, device="cuda").view(B, wide))
+        g = gen(150 + n)
+        k = (torch.randn(B * n, Hkv, d, generator=g) * 37).to(dt).cuda()
+        q = torch.randn(B * n, Hq, d, generator=g).to(dt).cuda()
+        rope = nsa.rope_table(T, rot)
+        past = [page * (b % 20) for b in range(B)]  # each begins a page
+        at = torch.tensor([past[b] + i for b in range(B) for i in range(n)]).cuda()
+        cu = None if n == 1 else i32([n * b for b in range(B + 1)])
+        q_out, _, _ = nsa.nsa_append_q8(p, k, k, i32(past), cache, cu_new=cu, q=q, rope=rope, rope_style=style)
+        nsa.nsa_check()
+        assert torch.equal(q_out, turned_fp32(q.float(), rope, at, style).to(dt))
+        want = turned_fp32(k.float(), rope, at, style).view(B, n, Hkv, d)
+        for b in range(B):
+            for j in range(0, n, page):
+                x = want[b, j:j + page]
+                pid = int(cache.page_table[b, (past[b] + j) // page])
+                for h in range(Hkv):
+                    s = ref.need(float(x[:, h].abs().max()))
+                    assert float(cache.k_scale[pid, h]) == s
+                    codes = (x[:, h] / s).to(torch.float8_e4m3fn).view(torch.uint8)
+                    assert torch.equal(cache.k_pages.view(torch.uint8)[pid, h, :len(x)], codes)
+
+
 @pytest.mark.parametrize("offsets", (False, True))
 def test_append_recodes_zeros_of_any_scale(offsets):
     """Stale slots of a page begun anew: zeros stay zeros under every scale, and
