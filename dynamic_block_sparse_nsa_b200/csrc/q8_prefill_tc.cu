@@ -386,6 +386,10 @@ struct Converter {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           x[k] = *reinterpret_cast<const uint4*>(sm.raw[r] + row(k) * D + (lane & 7) * 16);
+        // The next write to the slot is a bulk copy, of the async proxy: without the
+        // fence it can overtake these loads, whose data nothing has used yet (one
+        // call in 50 of 2600 queries had codes of the copy in place of V's).
+        ptx::fence_proxy_async();
         ptx::mbar_arrive(&B.raw_empty[r]);
         if (key0 + CK > all_hi || key0 < all_lo || live != (1u << (CK >> shift)) - 1) {
           // rows that no token sees hold anything: zeros

@@ -663,6 +663,32 @@ def test_prefill_matches_the_definition(case, keys):
         check_attention((out, lse), p, q, cache, i32(lens), cu.cpu(), keys)
 
 
+@pytest.mark.parametrize("past,new,keys", (
+    ([100, 0, 7, 1900], [650] * 4, "all"),
+    ([100, 0, 7, 1900], [650] * 4, "window"),
+    ([577], [2600], "all"),
+    ([0] * 4, [1040, 260, 520, 780], "all"),
+    ([1500 + 90 * b for b in range(24)], [1 + b % 7 for b in range(24)], "all"),
+), ids=str)
+def test_prefill_repeats_its_bits(past, new, keys):
+    """Many calls that fill the machine, each with the first one's bits. (A slot that
+    was copied into while its codes were still being read showed in one call of 50.)"""
+    B, N = len(new), sum(new)
+    lens = [a + n for a, n in zip(past, new)]
+    p = nsa.params(B, max(lens), 64, 4, 128, sel_block=64, window=200)
+    cache = random_cache(p, lens, 46, extra=0, spread=0.0)
+    q = torch.randn(N, 64, 128, generator=gen(47)).to(BF16).cuda()
+    cu = i32([0] + torch.tensor(new).cumsum(0).tolist())
+    L, ws = i32(lens), nsa.workspace(p, nsa.OP_PREFILL_Q8)
+    first = nsa.nsa_prefill_q8(p, q, cache, L, cu, keys=keys, ws=ws)
+    differ = 0
+    for _ in range(150):
+        got = nsa.nsa_prefill_q8(p, q, cache, L, cu, keys=keys, ws=ws)
+        differ += not (torch.equal(got[0], first[0]) and torch.equal(got[1], first[1]))
+    nsa.nsa_check()
+    assert differ == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv,lens,new", (
     (16, 1, [9000], [4]),                      # one unit over every block
     (16, 2, [70] * 200, [2] * 200),            # many units of one chunk
