@@ -400,9 +400,14 @@ struct Rows {
       if (PARTS == 1 && __vmaxu2(m2, 0x7f7f7f7fu) == 0x7f7f7f7fu) {  // all finite
         big = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
       } else {
+        // (an infinite component makes every score infinite or NaN: the row is NaN)
 #pragma unroll
-        for (int j = 0; j < D / 4; ++j)
-          if (fabsf(x[j]) < INFINITY) big = fmaxf(big, fabsf(x[j]));
+        for (int j = 0; j < D / 4; ++j) {
+          if (fabsf(x[j]) < INFINITY)
+            big = fmaxf(big, fabsf(x[j]));
+          else
+            x[j] = __uint_as_float(0x7fffffffu);
+        }
       }
       big = quad_max(big);
       // 2^up brings the largest component to [2^14, 2^15)
@@ -420,9 +425,7 @@ struct Rows {
           q[0][s][i + 2 * w] = hi2;
           if (PARTS == 2) {
             const float2 f = unpack_half(hi2);
-            // (an infinite component has no second part)
-            q[PARTS - 1][s][i + 2 * w] =
-                pack_half(fabsf(u0) < INFINITY ? u0 - f.x : 0.f, fabsf(u1) < INFINITY ? u1 - f.y : 0.f);
+            q[PARTS - 1][s][i + 2 * w] = pack_half(u0 - f.x, u1 - f.y);
           }
         }
     }

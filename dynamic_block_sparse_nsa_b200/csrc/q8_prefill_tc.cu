@@ -525,6 +525,7 @@ struct Softmax {
 #pragma unroll
     for (int c = 0; c < 16; ++c) x[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
     float big = 0.f;
+    bool finite = true;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -534,13 +535,16 @@ struct Softmax {
         const float f1 = fabsf(__uint_as_float(w[i] & 0xffff0000u));
         if (f0 < INFINITY) big = fmaxf(big, f0);
         if (f1 < INFINITY) big = fmaxf(big, f1);
+        finite &= f0 < INFINITY && f1 < INFINITY;
       }
     }
     // 2^up brings the largest component to [2^14, 2^15)
     int up = big > 0.f ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
     up = min(max(up, -120), 120);
     // (a negative softmax scale's sign goes into q)
-    const float mul = a.scale_log2 < 0.f ? -q8::exp2_int(up) : q8::exp2_int(up);
+    float mul = a.scale_log2 < 0.f ? -q8::exp2_int(up) : q8::exp2_int(up);
+    // (an infinite component makes every score infinite or NaN: the row is NaN)
+    if (!finite) mul = __uint_as_float(0x7fffffffu);
     qf = q8::exp2_int(-up) * fabsf(a.scale_log2);
     unsigned char* dst = sm.q[t] + row * 128;
 #pragma unroll

@@ -377,7 +377,8 @@ typedef enum { NSA_KEYS_ALL = 0, NSA_KEYS_WINDOW = 1, NSA_KEYS_BLOCKS = 2 } nsa_
  * A query without keys gives 0 and -inf. A length outside [0, T] does too and
  * sets the device error word; the tokens of a page whose number is outside
  * [0, num_pages) are left out, and set it. NaN components of keys and values
- * reach the queries that attend to them and no others.
+ * reach the queries that attend to them and no others; a query with a NaN or an
+ * infinite component gives NaN where it has keys.
  * Sums are fp32; a weight, times its page's value scale, is an fp16 number (two
  * for fp32 queries) in units that follow the row's largest product of a weight and
  * a value, so that a scale set by tokens that a query does not see changes nothing.

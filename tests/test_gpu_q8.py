@@ -969,6 +969,41 @@ def test_captured_chunks_serve_other_lengths(dt, Hq, Hkv, page, N):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("dt,d,page,G", ((BF16, 128, 64, 16), (BF16, 64, 16, 4), (F32, 64, 32, 4), (F32, 128, 128, 3)), ids=str)
+def test_queries_with_infinite_components(dt, d, page, G):
+    """Every score of such a query is infinite or NaN, and so its softmax NaN, whatever
+    the scores' signs; its neighbours keep theirs, and without keys it has 0 and -inf."""
+    p = nsa.params(3, 200, G, 1, d, sel_block=page, dtype=dt, window=150)
+    cache = random_cache(p, [200, 150, 0], 170)
+    codes = cache.k_pages.view(torch.uint8)
+    codes[..., 5] = 0x38 | 0x80  # component 5 of every key is negative
+    codes[..., 6] = 0x38         # component 6 positive
+    for bad in ({5: math.inf}, {6: -math.inf}, {5: -math.inf}, {5: math.inf, 6: -math.inf}, {7: math.nan}):
+        n = 40
+        q = torch.randn(2 * n, G, d, generator=gen(171)).to(dt)
+        clean = q.clone().cuda()
+        for r, h in ((0, 0), (17, G - 1), (n + 3, 1)):
+            for e, x in bad.items():
+                q[r, h, e] = x
+        q, lens, cu = q.cuda(), i32([200, 150, 0]), i32([0, n, 2 * n, 2 * n])
+        hit = torch.zeros(2 * n, G, dtype=torch.bool)
+        hit[0, 0] = hit[17, G - 1] = hit[n + 3, 1] = True
+        for keys in ("all", "window"):
+            want = nsa.nsa_prefill_q8(p, clean, cache, lens, cu, keys=keys)
+            out, lse = nsa.nsa_prefill_q8(p, q, cache, lens, cu, keys=keys)
+            nsa.nsa_check()
+            assert torch.equal(torch.isnan(out).all(-1).cpu(), hit) and torch.equal(torch.isnan(lse).cpu(), hit)
+            assert torch.equal(out[~hit.cuda()], want[0][~hit.cuda()])
+            assert torch.equal(lse[~hit.cuda()], want[1][~hit.cuda()])
+            one = q[[0, n + 3, 0]].contiguous()
+            out, lse = nsa.nsa_decode_q8(p, one, cache, lens, keys=keys)
+            nsa.nsa_check()
+            assert torch.isnan(out[0, 0]).all() and torch.isnan(out[1, 1]).all()
+            assert torch.isnan(lse[0, 0]) and torch.isnan(lse[1, 1])
+            assert torch.isfinite(out[0, 1:]).all() and torch.isfinite(out[1, 2:]).all()
+            assert not out[2].any() and (lse[2] == -math.inf).all()
+
+
 # ---- value scales that are none of a query's own ------------------------------------
 
 def outlier_cache(p, lens, seed, at, ratio, held=True):
