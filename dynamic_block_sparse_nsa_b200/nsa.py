@@ -441,27 +441,32 @@ def moba_prefill(p, q, k, v, out=None, sel_idx=None, ws=None, stream=None, want_
 class Q8Cache:
     """An 8-bit paged KV cache (include/nsa.h): k_pages, v_pages [P, Hkv, page, d]
     float8_e4m3fn, k_scale, v_scale [P, Hkv] fp32, page_table [B, max_pages] int32.
-    The tensors are the caller's and may be written between calls."""
+    The tensors are the caller's and may be written between calls; another tensor
+    is set by assignment, which checks it as the constructor does."""
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table):
+        self._set(dict(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale,
+                       page_table=page_table))
+
+    def _set(self, t):
+        k_pages = t["k_pages"]
         _dev(k_pages, "k_pages", torch.float8_e4m3fn)
         dev = k_pages.device
-        _dev(v_pages, "v_pages", torch.float8_e4m3fn, dev)
-        _dev(k_scale, "k_scale", torch.float32, dev)
-        _dev(v_scale, "v_scale", torch.float32, dev)
-        _dev(page_table, "page_table", torch.int32, dev)
-        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        _dev(t["v_pages"], "v_pages", torch.float8_e4m3fn, dev)
+        _dev(t["k_scale"], "k_scale", torch.float32, dev)
+        _dev(t["v_scale"], "v_scale", torch.float32, dev)
+        _dev(t["page_table"], "page_table", torch.int32, dev)
+        if k_pages.dim() != 4 or t["v_pages"].shape != k_pages.shape:
             raise ValueError("k_pages and v_pages must be [P, Hkv, page, d], of one shape")
-        if k_scale.shape != k_pages.shape[:2] or v_scale.shape != k_pages.shape[:2]:
+        if t["k_scale"].shape != k_pages.shape[:2] or t["v_scale"].shape != k_pages.shape[:2]:
             raise ValueError("k_scale and v_scale must be [P, Hkv]")
-        if page_table.dim() != 2:
+        if t["page_table"].dim() != 2:
             raise ValueError("page_table must be [B, max_pages]")
-        self.k_pages, self.v_pages = k_pages, v_pages
-        self.k_scale, self.v_scale, self.page_table = k_scale, v_scale, page_table
+        self._t = t
         self.device = dev
         self._p = None  # the parameters last found to fit
-        self.c = NsaQ8Cache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-                            v_scale.data_ptr(), page_table.data_ptr(), k_pages.shape[0])
+        self.c = NsaQ8Cache(*(t[n].data_ptr() for n in ("k_pages", "v_pages", "k_scale", "v_scale",
+                                                        "page_table")), k_pages.shape[0])
         self.ref = ctypes.byref(self.c)
 
     def _fits(self, p):
@@ -475,6 +480,15 @@ class Q8Cache:
             raise ValueError(f"page_table is {tuple(self.page_table.shape)}, the parameters need "
                              f"{(p.B, -(-p.T // p.sel_block))}")
         self._p = need
+
+    def _tensor(name):
+        return property(lambda self: self._t[name],
+                        lambda self, t: self._set({**self._t, name: t}))
+
+    k_pages, v_pages = _tensor("k_pages"), _tensor("v_pages")
+    k_scale, v_scale = _tensor("k_scale"), _tensor("v_scale")
+    page_table = _tensor("page_table")
+    del _tensor
 
 
 def q8_cache(p, num_pages, page_table):

@@ -1257,6 +1257,30 @@ def test_a_given_stream_owns_what_a_call_makes(monkeypatch):
     nsa.nsa_check()
 
 
+def test_cache_tensors_set_anew():
+    """An assigned tensor is the one that calls use; one that does not fit is refused."""
+    p = nsa.params(2, 100, 4, 2, 64, sel_block=32)
+    cache, other = random_cache(p, [100, 50], 180), random_cache(p, [100, 50], 181)
+    assert cache.k_pages.shape == other.k_pages.shape
+    q = torch.randn(2, 4, 64, generator=gen(182)).to(BF16).cuda()
+    lens = i32([100, 50])
+    want = nsa.nsa_decode_q8(p, q, other, lens)
+    for name in ("page_table", "k_pages", "v_pages", "k_scale", "v_scale"):
+        setattr(cache, name, getattr(other, name))
+        assert getattr(cache, name) is getattr(other, name)
+    got = nsa.nsa_decode_q8(p, q, cache, lens)
+    nsa.nsa_check()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for name, bad, text in (("page_table", i32([1, 2]), "page_table"), ("k_scale", other.k_scale[:1], "k_scale"),
+                            ("v_pages", other.v_pages.float(), "v_pages")):
+        with pytest.raises(ValueError, match=text):
+            setattr(cache, name, bad)
+        assert getattr(cache, name) is getattr(other, name)
+    cache.page_table = i32([[0, 1, 2, 3, 4]] * 2)  # more pages than the parameters have
+    with pytest.raises(ValueError, match="page_table"):
+        nsa.nsa_decode_q8(p, q, cache, lens)
+
+
 def test_wrapper_refusals():
     p = nsa.params(2, 100, 4, 2, 64, sel_block=32)
     cache = random_cache(p, [100, 50], 70)
