@@ -266,7 +266,7 @@ struct Feeder {
   // Whether the value scales of the unit's pages lie far apart, those just looked
   // up among them. `range`: the warp's, log2 of the least and the largest so far.
   __device__ __forceinline__ bool far(int* range, bool begun, int lane) const {
-    const int level = __float2int_rd(__log2f(vs));
+    const int level = max(-kFar, __float2int_rd(__log2f(vs)));
     int low = __reduce_min_sync(0xffffffffu, pid >= 0 && level > (int)q8::kSmall ? level : kFar);
     int high = __reduce_max_sync(0xffffffffu, pid >= 0 ? level : -kFar);
     if (begun) {

@@ -832,7 +832,7 @@ struct Softmax {
         const bool mine = lane < CK >> shift;
         const bool edge = (mine && pg.pid < 0) || key0 < lo || key0 + CK > hi;
         const bool there = mine && pg.pid >= 0;
-        const int level = __float2int_rd(pg.lv);
+        const int level = max(-kFar, __float2int_rd(pg.lv));
         // keys that some row does not see; or, rarely after a unit's first chunk,
         // scales beyond those before, or the smallest ones
         bool masked = __any_sync(0xffffffffu, edge || (there && (level < low || level > high)));

@@ -1070,6 +1070,47 @@ def test_prefill_unseen_outlier_values(dt, d, page, ratio):
             check_attention(got, p, q, cache, lens, cu.cpu(), keys)
 
 
+@pytest.mark.parametrize("dt,d,page,Hq,Hkv", ((BF16, 128, 64, 40, 2), (BF16, 128, 32, 6, 2), (F32, 128, 16, 6, 2),
+                                              (BF16, 64, 128, 20, 1)), ids=str)
+def test_nan_values_among_scales_far_apart(dt, d, page, Hq, Hkv):
+    """NaN values in pages of scales 2^-120 to 2^110: the rows that see them, no others;
+    pages of zeros of any scale, and rows whose keys are all in such pages."""
+    lens, new = [500, 333, 700], [90, 20, 60]
+    p = nsa.params(3, 720, Hq, Hkv, d, sel_block=page, dtype=dt, window=140)
+    N, g = sum(new), gen(99)
+    cache = random_cache(p, lens, 100, spread=0.0)
+    pages = cache.v_scale.shape[0]
+    cache.v_scale.copy_(torch.exp2(torch.randint(-120, 111, (pages, Hkv), generator=g).float()))
+    zero = torch.rand(pages, Hkv, generator=g) < 0.4
+    table = cache.page_table.cpu()
+    last = [int(x) for x in table[1] if x >= 0]
+    zero[last] = True                       # sequence 1 has nothing but zeros
+    live = cache.v_pages.view(torch.uint8)
+    live.copy_(torch.where(zero[..., None, None].cuda(), 0, live))
+    q = torch.randn(N, Hq, d, generator=g).to(dt).cuda()
+    cu = i32([0, 90, 110, 170])
+    for keys in ("all", "window"):
+        got = nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu, keys=keys)
+        nsa.nsa_check()
+        want, wlse, A, B = ref.attend(q, cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+                                      cache.page_table, i32(lens), page, cu.cpu(), keys, p.window)
+        t_out, t_lse = ref.bounds(want, wlse, A, B, dt, 700)
+        # (beside the relative bound: a weight's last place next to the row's largest
+        # product, 2^-21 of it a key where codes may be as small as here)
+        t_out = t_out + 700 * 2.0 ** -21 * A.amax(-1, keepdim=True)
+        assert ((got[0].double().cpu() - want).abs() <= t_out).all()
+        assert ((got[1].double().cpu() - wlse).abs() <= t_lse).all()
+        assert not got[0][90:110].any()
+    base = nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu)
+    want = nan_marks(p, cache, lens, new, [470, 320, 100], [3, 5, 7])
+    out, lse = nsa.nsa_prefill_q8(p, q, cache, i32(lens), cu)
+    nsa.nsa_check()
+    assert torch.equal(torch.isnan(out).cpu(), want) and torch.equal(lse, base[1])
+    # (a code less may change the units that sums are held in)
+    scale = base[0].abs().amax(-1, keepdim=True).expand_as(out)[~want.cuda()].double()
+    assert ((out - base[0]).abs()[~want.cuda()].double() <= scale * 2.0 ** -7).all()
+
+
 def test_prefill_drafts_unseen_outlier_values():
     """Few queries a sequence over many keys, where both tile halves share the keys."""
     B, new = 20, 4
