@@ -21,7 +21,7 @@
 // (0, 1024] and its smallest normal 2^-24 below the largest). A scale says
 // little of what a row sees: it may be that of a later token, of one before the
 // window, or of one written over since. So once the scales of a warp's pages lie
-// more than 2^8 apart, M is the largest p * max |v| of a single key instead, and
+// too far apart (q8::spread), M is the largest p * max |v| of a single key instead, and
 // falls to what o holds where an earlier page had set it too high (apart_softmax).
 //
 // Each warp streams its own contiguous share of the chunks (64 keys) through a
@@ -265,7 +265,7 @@ struct Feeder {
 
   // Whether the value scales of the unit's pages lie far apart, those just looked
   // up among them. `range`: the warp's, log2 of the least and the largest so far.
-  __device__ __forceinline__ bool far(int* range, bool begun, int lane) const {
+  __device__ __forceinline__ bool far(int* range, bool begun, int spread, int lane) const {
     const int level = max(-kFar, __float2int_rd(__log2f(vs)));
     int low = __reduce_min_sync(0xffffffffu, pid >= 0 && level > (int)q8::kSmall ? level : kFar);
     int high = __reduce_max_sync(0xffffffffu, pid >= 0 ? level : -kFar);
@@ -278,7 +278,7 @@ struct Feeder {
       range[0] = low;
       range[1] = high;
     }
-    return high - low > (int)q8::kSpread;
+    return high - low > spread;
   }
 
   // Copies K or V of the chunk into a slot.
@@ -902,7 +902,7 @@ __device__ __forceinline__ bool share(const Q8AttendArgs& a, const Plan& pl, uns
     ptx::cp_async_commit();
     rows.load(raw, a, u, lane);
     feed.scales(meta, lane);
-    if (!FAR && feed.far(range, false, lane)) {
+    if (!FAR && feed.far(range, false, q8::spread<T>(), lane)) {
       ptx::cp_async_wait<0>();  // (the ring is used anew)
       __syncwarp();
       return false;
@@ -925,7 +925,8 @@ __device__ __forceinline__ bool share(const Q8AttendArgs& a, const Plan& pl, uns
     }
     ptx::cp_async_commit();
     if (more) feed.scales(meta + (mi ^ 1), lane);
-    if (!FAR && more && feed.centry == feed.gbase && feed.far(range, feed.at.c > 0, lane)) {
+    if (!FAR && more && feed.centry == feed.gbase &&
+        feed.far(range, feed.at.c > 0, q8::spread<T>(), lane)) {
       ptx::cp_async_wait<0>();  // (the ring is used anew)
       __syncwarp();
       return false;

@@ -25,11 +25,17 @@ enum { KEYS_ALL = NSA_KEYS_ALL, KEYS_WINDOW = NSA_KEYS_WINDOW, KEYS_BLOCKS = NSA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Value scales of a unit's pages that lie further apart than 2^kSpread ("far
-// apart"): the output's reference M is then taken from the codes that a row sees
-// and from its sums, not from the scales, which other tokens may have set. Scales
-// up to 2^kSmall do not count: no value under them reaches 1e-30.
-constexpr float kSpread = 8.f, kSmall = -109.f;
+// Value scales of a unit's pages that lie further apart than 2^spread ("far apart"):
+// the output's reference M is then taken from the codes that a row sees and from its
+// sums, not from the scales, which other tokens may have set. Up to there a weight's
+// smallest place in fp16 lies at least 2^(35 - spread) below the row's largest
+// weight; 2^27 for fp32 rows and 2^23 for bf16 ones, 2^3 and 2^14 beyond their types' places. Scales up
+// to 2^kSmall do not count: no value under them reaches 1e-30.
+template <typename T>
+constexpr int spread() {
+  return sizeof(T) == 4 ? 8 : 12;
+}
+constexpr float kSmall = -109.f;
 
 // Places, 0 to 5, by which the largest magnitude c of a key's value codes lies
 // below 2^8: a weight may be that much larger beside it in fp16. kNoCode: zeros.

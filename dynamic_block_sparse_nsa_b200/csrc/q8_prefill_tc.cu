@@ -853,7 +853,7 @@ struct Softmax {
         wait(&B.s_full[t], tiles++, abort, a.err);
         tc::fence_after_sync();
         const uint32_t sc = tl + s_col(t);
-        const bool far = high - low > (int)q8::kSpread;
+        const bool far = high - low > q8::spread<__nv_bfloat16>();
         const int kv = kv0 + 2 * i + (split && i < chunks - 1 ? 2 : 1);  // the chunk's V tile
         // (a call here: inline, here or below, the split kernel's chunks take 4 to 9 %
         // longer; the other's take 3 % longer with it, and 1 % less as below)

@@ -382,11 +382,11 @@ typedef enum { NSA_KEYS_ALL = 0, NSA_KEYS_WINDOW = 1, NSA_KEYS_BLOCKS = 2 } nsa_
  * Sums are fp32; a weight, times its page's value scale, is an fp16 number (two
  * for fp32 queries) in units that follow the row's largest product of a weight and
  * a value, so that a scale set by tokens that a query does not see changes nothing.
- * Besides its relative rounding, a weight has an error of up to 2^-27 of the row's
- * largest (2^-35 where the value scales are alike). Where they lie more than 2^8
- * apart, that is up to 2^-33 (2^-21 beside codes near e4m3's smallest) of the
- * largest product of a weight and a component that the row sees, for each key in
- * out. Values below 1e-30 may count as zero.
+ * Besides its relative rounding, a weight has an error of up to 2^-35 of the row's
+ * largest where the value scales are alike, and up to 2^-23 (fp32 queries: 2^-27)
+ * where they lie up to 2^12 (2^8) apart. Beyond, it is up to 2^-33 (2^-21 beside
+ * codes near e4m3's smallest) of the largest product of a weight and a component
+ * that the row sees, for each key in out. Values below 1e-30 may count as zero.
  *   workspace  nsa_workspace_size(NSA_OP_DECODE_Q8) bytes; calls that may
  *              overlap on the GPU need one each. */
 NSA_API nsa_status nsa_decode_q8(const nsa_params* p, const nsa_q8_cache* cache, const void* q,

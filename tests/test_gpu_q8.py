@@ -1024,7 +1024,7 @@ OUTLIERS = ((BF16, 128, 64), (BF16, 128, 32), (BF16, 64, 16), (F32, 64, 16), (F3
 
 
 @pytest.mark.parametrize("dt,d,page", OUTLIERS, ids=str)
-@pytest.mark.parametrize("ratio", (2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100))
+@pytest.mark.parametrize("ratio", (2.0 ** 7, 2.0 ** 10, 2.0 ** 12, 2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100))
 def test_decode_unseen_outlier_values(dt, d, page, ratio):
     """A value that a query does not see, in a page of which it sees other tokens, takes
     nothing from the query's sums, however large: a token before the window, one
@@ -1054,7 +1054,7 @@ def test_decode_unseen_outlier_values(dt, d, page, ratio):
 
 
 @pytest.mark.parametrize("dt,d,page", OUTLIERS, ids=str)
-@pytest.mark.parametrize("ratio", (2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100))
+@pytest.mark.parametrize("ratio", (2.0 ** 7, 2.0 ** 10, 2.0 ** 12, 2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100))
 def test_prefill_unseen_outlier_values(dt, d, page, ratio):
     """The same for chunks: queries before the outlier's token, and those whose window
     has left it, keep their sums; the others have its value."""
