@@ -11,8 +11,8 @@
 // become halves exactly (e4m3 is a subset of fp16). fp32 rows are kept as two
 // halves each, q = hi + lo and p = hi + lo (22 significant bits), bf16 rows as
 // one: q is scaled by a power of two per row into the top of fp16's range, so
-// its 8 bits stay exact, and p's rounding (2^-12 relative) is below that of
-// the bf16 output (2^-9).
+// its 8 bits stay exact, and p's rounding (2^-11 relative) is below that of
+// the bf16 output (2^-8).
 //
 // A page's value scale multiplies p before p is rounded to half. So that no
 // spread of scales over the pages can push it out of fp16's range, the output
@@ -35,13 +35,19 @@
 //
 // Measured, 64 query heads on 4 KV heads, d = 128, bf16: one query of each of 32
 // sequences of 65536 tokens 330 us, 6.5 TB/s of codes, the rate of a copy; in
-// long runs of such calls 392 us, at the board's power limit. A short call is
-// one or two passes of a warp (some 4250 instructions, no loop to warm the
-// instruction cache) between start and join: 1000 tokens 14.6 us, of 0.16 for
-// the bytes. fp32 does each product twice and splits every p: 24 sequences of up
-// to 9001 tokens (40 heads on 8, d = 64) 54 us of 17. What was measured slower:
-// prefetches of pages into L2 (518 us), chunks of 32 keys (531 us), twelve warps
-// a block (fp32 64 us), one copy of the loop's body for both kinds of chunk (350).
+// long runs of such calls 375 to 390 us, at the board's power limit. A short call
+// is latency: of one key 8.6 us (1.7 of it an empty kernel's; lengths, plan, page,
+// scale, codes and query one behind the other, and instructions that no loop has
+// warmed the cache with, which are most of its stalls), 2 to 3 for the join of a
+// block's warps and as much for a second pass of them: 1000 tokens 14.8 us, of 0.16
+// for the bytes. fp32 does each product twice and splits every p, and eight warps
+// do not hide the latencies between (issue slots 30 % used, tensor pipe 26 %): 24
+// sequences of up to 9001 tokens (40 heads on 8, d = 64) 56 us of 17. More than 16
+// heads to a KV head read the codes once for every 16. Value scales too far apart
+// take 2 to 2.5 times as long (32 x 16384 tokens 99 and 244 us); the look-out for
+// them costs bf16 calls 0 to 3 %, fp32 ones 2 to 5. What was measured slower:
+// prefetches of pages into L2 (518 us), chunks of 32 keys (531 us), twelve warps a
+// block (fp32 64 us), one copy of the loop's body for both kinds of chunk (350).
 #include <algorithm>
 
 #include "q8_attend.cuh"

@@ -19,11 +19,14 @@
 //                    half's products do.
 // Where most sequences have rows for one half only (draft tokens), both halves
 // take the same rows and alternate chunks (SPLIT), and half 0 joins the two sums
-// at the unit's end: 16 sequences of 4 queries over 8191 keys 93 -> 75 us (a
-// chunk 1.33 us instead of 2.4; plan, start and merge are some 30 us of it).
+// at the unit's end: 16 sequences of 4 queries over 8191 keys 93 -> 75 us when it
+// came in, 77 with the fence behind the converters' loads (a chunk 1.4 us instead
+// of 2.4; with one chunk a sequence the call takes 22 us: plan, start and merge).
 // A half's chain of softmax (an exponential for every score, 16 a clock and SM,
 // is as long as its two products) and products bounds it. 2048 queries of 64
-// heads over 16384 keys (4 KV heads): 1.04 ms, 990 TFLOP/s. What was measured
+// heads over 16384 keys (4 KV heads): 1.07 ms, 967 TFLOP/s, in short runs, 1.11 ms,
+// 929 TFLOP/s, in a program of such calls at the board's power limit. Value scales
+// too far apart (q8_attend.cuh) take five times as long. What was measured
 // slower: steps of 64 keys with two S tiles a half (the products' overhead
 // doubles: 1.15 ms), two threads a row (16 softmax warps: 1.05 ms, short units
 // 87 us), 192 registers for the softmax by setmaxnreg (the other

@@ -363,7 +363,8 @@ NSA_API nsa_status nsa_append_q8(const nsa_params* p, const nsa_q8_cache* cache,
 typedef enum { NSA_KEYS_ALL = 0, NSA_KEYS_WINDOW = 1, NSA_KEYS_BLOCKS = 2 } nsa_keys;
 
 /* Single-token attention over the 8-bit cache: softmax(scale q . k) v of one
- * query per sequence over its keys, out of HBM bytes: the codes are read once.
+ * query per sequence over its keys. The codes are read once for every 16 heads of
+ * a KV head.
  *   q          [B, Hq, d] dtype: the query at position seq_lens[b] - 1.
  *   seq_lens   [B] int32, device, 0 <= seq_lens[b] <= T (0: no keys).
  *   keys       nsa_keys.
