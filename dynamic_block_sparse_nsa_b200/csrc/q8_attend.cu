@@ -21,8 +21,9 @@
 // (0, 1024] and its smallest normal 2^-24 below the largest). A scale says
 // little of what a row sees: it may be that of a later token, of one before the
 // window, or of one written over since. So once the scales of a warp's pages lie
-// too far apart (q8::spread), M is the largest p * max |v| of a single key instead, and
-// falls to what o holds where an earlier page had set it too high (apart_softmax).
+// too far apart (q8::spread), M is the largest p * max |v| of a single key instead,
+// and falls to what o holds where an earlier page had set it too high
+// (apart_softmax).
 //
 // Each warp streams its own contiguous share of the chunks (64 keys) through a
 // private ring of three cp.async slots, each K or V of a chunk, two of them in
@@ -465,7 +466,8 @@ struct Rows {
   }
 
   template <int PP>
-  __device__ __forceinline__ void mask(float (&z)[NS][4], const ChunkMeta<PP>& meta, int lane) const {
+  __device__ __forceinline__ void mask(float (&z)[NS][4], const ChunkMeta<PP>& meta,
+                                       int lane) const {
     const int t = lane & 3;
     constexpr int TP = NS / PP;
 #pragma unroll
@@ -514,7 +516,8 @@ struct Rows {
       for (int nt = 0; nt < NS; ++nt)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          room[y] |= __shfl_sync(0xffffffffu, nt < NS / 2 ? a : b, (8 * nt + t + 4 * y) % 32) << 4 * nt;
+          room[y] |= __shfl_sync(0xffffffffu, nt < NS / 2 ? a : b, (8 * nt + t + 4 * y) % 32)
+                     << 4 * nt;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -28,9 +28,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Value scales of a unit's pages that lie further apart than 2^spread ("far apart"):
 // the output's reference M is then taken from the codes that a row sees and from its
 // sums, not from the scales, which other tokens may have set. Up to there a weight's
-// smallest place in fp16 lies at least 2^(35 - spread) below the row's largest
-// weight; 2^27 for fp32 rows and 2^23 for bf16 ones, 2^3 and 2^14 beyond their types' places. Scales up
-// to 2^kSmall do not count: no value under them reaches 1e-30.
+// smallest place in fp16 lies at least 2^(35 - spread) below the row's largest weight:
+// 2^27 for fp32 rows, 2^23 for bf16 ones, 2^3 and 2^14 beyond their types' places.
+// Scales up to 2^kSmall do not count: no value under them reaches 1e-30.
 template <typename T>
 constexpr int spread() {
   return sizeof(T) == 4 ? 8 : 12;

@@ -1262,6 +1262,36 @@ def test_two_streams_with_their_own_workspaces():
     nsa.nsa_check()
 
 
+def test_two_streams_of_chunks():
+    """Chunks of two caches at once, on streams and workspaces of their own, between
+    appends of one and the other: the bits of one stream alone."""
+    T, new = 2400, [400, 300, 500]
+    p = nsa.params(3, T, 64, 4, 128, sel_block=64)
+    rope, N = nsa.rope_table(T, 128), sum(new)
+    past, cu = i32([1900, 0, 1000]), i32([0, 400, 700, 1200])
+    lens = i32([2300, 300, 1500])
+    parts = []
+    for x in range(2):
+        g = gen(190 + x)
+        q, k, v = (torch.randn(N, h, 128, generator=g).to(BF16).cuda() for h in (64, 4, 4))
+        parts.append((random_cache(p, [2300, 300, 1500], 192 + x), q, k, v, nsa.workspace(p, nsa.OP_PREFILL_Q8),
+                      torch.cuda.Stream()))
+
+    def run(part, stream):
+        cache, q, k, v, ws, _ = part
+        rot, _, _ = nsa.nsa_append_q8(p, k, v, past, cache, cu_new=cu, q=q, rope=rope, stream=stream)
+        return nsa.nsa_prefill_q8(p, rot, cache, lens, cu, ws=ws, stream=stream)
+
+    want = [run(part, None) for part in parts]
+    torch.cuda.synchronize()
+    got = [[run(part, part[-1]) for part in parts] for _ in range(30)]
+    torch.cuda.synchronize()
+    nsa.nsa_check()
+    for pair in got:
+        for (out, lse), (o, s) in zip(pair, want):
+            assert torch.equal(out, o) and torch.equal(lse, s)
+
+
 def test_a_given_stream_owns_what_a_call_makes(monkeypatch):
     """As tests/test_gpu_nsa.py's: outputs and workspaces made for a call on a stream."""
     from tests.test_gpu_nsa import _owner
