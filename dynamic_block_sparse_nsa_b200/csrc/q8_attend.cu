@@ -36,7 +36,7 @@
 //
 // Measured, 64 query heads on 4 KV heads, d = 128, bf16: one query of each of 32
 // sequences of 65536 tokens 330 us, 6.5 TB/s of codes, the rate of a copy; in
-// long runs of such calls 375 to 390 us, at the board's power limit. A short call
+// long runs of such calls 370 to 400 us, at the board's power limit. A short call
 // is latency: of one key 8.6 us (1.7 of it an empty kernel's; lengths, plan, page,
 // scale, codes and query one behind the other, and instructions that no loop has
 // warmed the cache with, which are most of its stalls), 2 to 3 for the join of a
